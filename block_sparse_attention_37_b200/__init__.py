@@ -23,6 +23,7 @@ BLOCK_NONE, BLOCK_FULL, BLOCK_PARTIAL = 0, 1, 2
 MASK_ARROW, MASK_GNA = 1, 2
 SELECT_POOLED_QK, SELECT_FULL_SCORE = 1, 2
 STEP_FULL, STEP_SELECT, STEP_REUSE = 0, 1, 2
+CACHE_BF16, CACHE_E4M3 = 1, 2
 
 EXPORTS = (
     "bsa_version", "bsa_error_string", "bsa_build_mask", "bsa_select_workspace_size",
@@ -30,6 +31,7 @@ EXPORTS = (
     "bsa_unpermute_tiles", "bsa_get_device_error", "bsa_select_topk_static", "bsa_rse",
     "bsa_plan_heads", "bsa_schedule_full_steps", "bsa_step_action", "bsa_keep_pct", "bsa_jaccard",
     "bsa_set_wait_limit_ns", "bsa_set_withheld_tile", "bsa_quantize_fp8", "bsa_forward_fp8",
+    "bsa_paged_append", "bsa_paged_read", "bsa_paged_workspace_size", "bsa_paged_forward",
 )
 STATIC_SCRATCH_BYTES = 16 << 20
 
@@ -81,6 +83,13 @@ class SelectSpec(ctypes.Structure):
                 ("keep_text", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class PagedCacheC(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("d", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p)]
+
+
 # ---------------------------------------------------------------------------- library
 
 _LIB = None
@@ -119,6 +128,11 @@ def _lib():
         lib.bsa_quantize_fp8.argtypes = [P] * 11
         lib.bsa_forward_fp8.argtypes = [P] * 13 + [ctypes.c_float, P, P]
         lib.bsa_set_withheld_tile.argtypes = [I32]
+        lib.bsa_paged_append.argtypes = [P] * 6
+        lib.bsa_paged_read.argtypes = [P] * 6
+        lib.bsa_paged_workspace_size.restype = ctypes.c_size_t
+        lib.bsa_paged_workspace_size.argtypes = [P, P]
+        lib.bsa_paged_forward.argtypes = [P, P, P, P, I32, I32, ctypes.c_float, P, ctypes.c_size_t, P, P]
         _LIB = lib
     return _LIB
 
@@ -362,6 +376,137 @@ def forward_fp8(dm: Dims, ops: Fp8Operands, o, head_mode, blocks: BlockList | No
                                   ctypes.byref(lc) if lc is not None else None, hm,
                                   ctypes.byref(gna) if gna is not None else None, ci, co, bp, float(scale), op,
                                   _stream(stream)), "bsa_forward_fp8")
+
+
+class PagedCache:
+    """Keys and values of several sequences in pages (see bsa_paged_cache): k and v are cuda
+    [n_pages, Hkv, page, d] bf16, or uint8 e4m3 codes with the fp32 scales k_scale and v_scale
+    [n_pages, Hkv, page]; table is int32 [B, max_pages], kv_len int32 [B]. The tensors are the
+    caller's: their contents may change between calls (pages filled, kv_len raised), the tensors
+    of a PagedCache may not."""
+    __slots__ = ("k", "v", "table", "kv_len", "k_scale", "v_scale", "device", "_c", "_ref")
+
+    def __init__(self, k, v, table, kv_len, k_scale=None, v_scale=None):
+        e4m3 = isinstance(k, torch.Tensor) and k.dtype == torch.uint8
+        dt = torch.uint8 if e4m3 else torch.bfloat16
+        for t, name in ((k, "k"), (v, "v"), (table, "table"), (kv_len, "kv_len")):
+            if t is None:
+                raise TypeError(f"{name} must be a torch.Tensor")
+        _check_buffer(k, dt, "k")
+        if k.dim() != 4:
+            raise ValueError("k must be [n_pages, Hkv, page, d]")
+        _check_buffer(table, torch.int32, "table")
+        if table.dim() != 2:
+            raise ValueError("table must be [B, max_pages]")
+        n_pages, Hkv, page, d = k.shape
+        for t, name, shape, dtype in ((v, "v", k.shape, dt), (kv_len, "kv_len", table.shape[:1], torch.int32),
+                                      (k_scale, "k_scale", k.shape[:3], torch.float32),
+                                      (v_scale, "v_scale", k.shape[:3], torch.float32)):
+            if name.endswith("scale") and (t is None) == e4m3:
+                raise TypeError(f"{name} is needed for an e4m3 cache" if e4m3
+                                else f"{name} belongs to an e4m3 cache (k and v uint8)")
+            if t is None:
+                continue
+            _check_buffer(t, dtype, name)
+            if t.shape != shape:
+                raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        p = _ptrs((k, dt, "k"), (v, dt, "v"), (k_scale, torch.float32, "k_scale"),
+                  (v_scale, torch.float32, "v_scale"), (table, torch.int32, "table"), (kv_len, torch.int32, "kv_len"))
+        for t, name in ((v, "v"), (table, "table"), (kv_len, "kv_len"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is not None and t.device != k.device:
+                raise ValueError(f"{name} is on {t.device}, k on {k.device}")
+        self.k, self.v, self.table, self.kv_len = k, v, table, kv_len
+        self.k_scale, self.v_scale, self.device = k_scale, v_scale, k.device
+        self._c = PagedCacheC(CACHE_E4M3 if e4m3 else CACHE_BF16, n_pages, Hkv, page, d, table.shape[1], *p)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, n_pages, Hkv, page, d, B, max_pages, kind=CACHE_BF16, device="cuda") -> "PagedCache":
+        """Pages without contents; table and kv_len zero."""
+        if kind not in (CACHE_BF16, CACHE_E4M3):
+            raise ValueError("kind must be CACHE_BF16 or CACHE_E4M3")
+        dt = torch.uint8 if kind == CACHE_E4M3 else torch.bfloat16
+        kv = lambda: torch.empty((n_pages, Hkv, page, d), dtype=dt, device=device)
+        sc = lambda: (torch.empty((n_pages, Hkv, page), dtype=torch.float32, device=device)
+                      if kind == CACHE_E4M3 else None)
+        return cls(kv(), kv(), torch.zeros((B, max_pages), dtype=torch.int32, device=device),
+                   torch.zeros((B,), dtype=torch.int32, device=device), sc(), sc())
+
+    def _chunk(self, dm: Dims) -> int:
+        """Elements of this call's [B, Hkv, N, d] chunk; refuses dims that are not the cache's."""
+        if dm.B != self.kv_len.shape[0]:
+            raise ValueError(f"dims hold {dm.B} sequences, the cache's table {self.kv_len.shape[0]}")
+        return dm.B * self._c.Hkv * max(dm.N, 0) * max(dm.d, 0)
+
+
+def _paged_ptr(cache: PagedCache, t, dtype, name, numel):
+    """_ptr for the calls on a cache, whose launches are short enough for the checks to show:
+    one test of everything, and _ptr to say what is wrong. The tensor must be on the cache's
+    device, which is made current for the call (see _on)."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.numel() >= numel and t.is_contiguous()
+            and t.device == cache.device and t.is_cuda):
+        return t.data_ptr()
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    p = _ptr(t, dtype, name, numel)
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    return p
+
+
+def _on(cache: PagedCache, where: str, call, stream):
+    """call(stream) with the cache's device current, on `stream` or that device's current stream."""
+    if cache.device.type == "cuda" and cache.device.index != torch.cuda.current_device():
+        with torch.cuda.device(cache.device):
+            return _check(call(_stream(stream)), where)
+    return _check(call(_stream(stream)), where)
+
+
+def paged_append(dm: Dims, cache: PagedCache, k, v, n_new=None, stream=None):
+    """bsa_paged_append: write a chunk's k and v (cuda bf16 [B, Hkv, N, d]) at the end of each
+    sequence, positions kv_len - n_new .. kv_len - 1 (set kv_len to the new lengths first).
+    n_new: cuda int32 [B], the chunk's tokens per sequence, or None (N each)."""
+    n = cache._chunk(dm)
+    kp, vp = _paged_ptr(cache, k, torch.bfloat16, "K", n), _paged_ptr(cache, v, torch.bfloat16, "V", n)
+    np_ = _paged_ptr(cache, n_new, torch.int32, "n_new", dm.B) if n_new is not None else None
+    lib = _lib()
+    _on(cache, "bsa_paged_append", lambda s: lib.bsa_paged_append(ctypes.byref(dm), kp, vp, np_, cache._ref, s), stream)
+
+
+def paged_read(dm: Dims, cache: PagedCache, k, v, begin=None, stream=None):
+    """bsa_paged_read: tokens begin .. begin + N - 1 of each sequence into k and v (cuda bf16
+    [B, Hkv, N, d]), zeros past its end. begin: cuda int32 [B], or None (0)."""
+    n = cache._chunk(dm)
+    kp, vp = _paged_ptr(cache, k, torch.bfloat16, "K", n), _paged_ptr(cache, v, torch.bfloat16, "V", n)
+    bp = _paged_ptr(cache, begin, torch.int32, "begin", dm.B) if begin is not None else None
+    lib = _lib()
+    _on(cache, "bsa_paged_read", lambda s: lib.bsa_paged_read(ctypes.byref(dm), cache._ref, bp, kp, vp, s), stream)
+
+
+def paged_workspace_size(dm: Dims, cache: PagedCache) -> int:
+    """Bytes of device workspace paged_forward needs for these dims and cache, whatever the lengths."""
+    return int(_lib().bsa_paged_workspace_size(ctypes.byref(dm), cache._ref))
+
+
+def paged_forward(dm: Dims, cache: PagedCache, q, o, workspace, n_new=None, causal: bool = True, window: int = 0,
+                  scale: float | None = None, stream=None):
+    """bsa_paged_forward: o (cuda bf16 [B, H, N, d]) = attention of a chunk's queries q over the
+    cached tokens, those of the chunk included (append first); H is a multiple of the cache's heads.
+    n_new: cuda int32 [B], the chunk's tokens per sequence (rows of o behind them are left as they
+    were), or None (N each). causal: row i keeps the keys up to its own position, with window > 0
+    the last `window` of them; otherwise every cached token. workspace: cuda tensor of at least
+    paged_workspace_size bytes, 256-byte aligned, not shared with a call that may overlap; scale
+    defaults to 1/sqrt(d)."""
+    scale = (1.0 / dm.d ** 0.5) if scale is None else scale
+    cache._chunk(dm)
+    n = _tokens(dm)
+    qp, op = _paged_ptr(cache, q, torch.bfloat16, "Q", n), _paged_ptr(cache, o, torch.bfloat16, "O", n)
+    np_ = _paged_ptr(cache, n_new, torch.int32, "n_new", dm.B) if n_new is not None else None
+    wp = _paged_ptr(cache, workspace, getattr(workspace, "dtype", None), "workspace", 0)
+    wb = workspace.numel() * workspace.element_size()
+    lib = _lib()
+    _on(cache, "bsa_paged_forward", lambda s: lib.bsa_paged_forward(
+        ctypes.byref(dm), qp, np_, cache._ref, 1 if causal else 0, window, float(scale), wp, wb, op, s), stream)
 
 
 def gna_tiled_len(n_text: int, gna: GnaGeom) -> int:

@@ -1,0 +1,77 @@
+// The paged key/value cache as the kernels see it, and their launchers.
+#pragma once
+
+#include "common.cuh"
+
+namespace bsa {
+
+struct PagedParams {
+  int B, H, Hkv, N, d;
+  int n_pages, max_pages, page_log2;
+  int e4m3;
+  uint8_t* k;  // [n_pages, Hkv, page, d], bf16 or e4m3 codes
+  uint8_t* v;
+  float* k_scale;  // [n_pages, Hkv, page], e4m3 only
+  float* v_scale;
+  const int32_t* table;   // [B, max_pages]
+  const int32_t* kv_len;  // [B]
+  const int32_t* n_new;   // [B] or null: N each (append, forward)
+  const int32_t* begin;   // [B] or null: 0 each (read)
+  __nv_bfloat16* new_k;   // [B, Hkv, N, d]: source of an append, destination of a read
+  __nv_bfloat16* new_v;
+  FastDiv f_n, f_hkv;
+  // forward
+  const __nv_bfloat16* Q;  // [B, H, N, d]
+  __nv_bfloat16* O;
+  int G;                   // query heads a key/value head
+  int causal, window;
+  float scale_log2;        // scale * log2(e)
+};
+
+// A sequence's chunk and cache lengths, clamped to what the arguments hold.
+struct SeqLen {
+  int n, kv;
+  bool bad;
+};
+
+__host__ __device__ __forceinline__ SeqLen clamp_lens(const PagedParams& p, int n, int kv) {
+  SeqLen s{n, kv, false};
+  const long long cap = (long long)p.max_pages << p.page_log2;
+  if (kv < 0 || kv > cap) {
+    s.bad = true;
+    s.kv = kv < 0 ? 0 : (int)cap;
+  }
+  if (n < 0 || n > p.N) {
+    s.bad = true;
+    s.n = n < 0 ? 0 : p.N;
+  }
+  return s;
+}
+
+__device__ __forceinline__ SeqLen seq_lens(const PagedParams& p, int b) {
+  const SeqLen s = clamp_lens(p, p.n_new ? __ldg(p.n_new + b) : p.N, __ldg(p.kv_len + b));
+  if (s.bad) record_error(BSA_DEVERR_BAD_INDEX);
+  return s;
+}
+
+// The page of position j of sequence b (j inside the table's row); -1, with
+// the fault recorded, for an index outside the cache.
+__device__ __forceinline__ int page_of(const PagedParams& p, int b, int j) {
+  const int pg = __ldg(p.table + (size_t)b * p.max_pages + (j >> p.page_log2));
+  if (pg < 0 || pg >= p.n_pages) {
+    record_error(BSA_DEVERR_BAD_INDEX);
+    return -1;
+  }
+  return pg;
+}
+
+// Row (token and head) index of slot j % page of page pg: rows hold d values.
+__host__ __device__ __forceinline__ long long cache_row(const PagedParams& p, int pg, int hk, int j) {
+  return (((long long)pg * p.Hkv + hk) << p.page_log2) + (j & ((1 << p.page_log2) - 1));
+}
+
+cudaError_t launch_paged_append(const PagedParams& p, cudaStream_t stream);
+cudaError_t launch_paged_read(const PagedParams& p, cudaStream_t stream);
+cudaError_t launch_paged_forward(const PagedParams& p, cudaStream_t stream);
+
+}  // namespace bsa

@@ -263,6 +263,99 @@ int bsa_forward_fp8(const bsa_dims* dims, const uint8_t* q8, const uint8_t* k8, 
                     const int32_t* head_mode, const bsa_gna_geom* gna, const float* cache_in,
                     float* cache_out, const float* block_bias, float scale, void* O, void* stream);
 
+/* ---- paged key/value cache ----------------------------------------------
+ * Keys and values of B sequences, kept between calls in pages of `page`
+ * tokens, for models that work against cached tokens: one token at a time, a
+ * block of tokens denoised at a time, or a prompt in chunks. Token j of
+ * sequence b lives in page table[b][j / page], slot j % page. The caller
+ * allocates pages, fills the table and keeps kv_len; the library only reads
+ * table and kv_len.
+ *
+ * kv_len[b] counts the cached tokens of sequence b, those of the current
+ * chunk included: of a chunk of n tokens, token i sits at position
+ * kv_len[b] - n + i. A chunk is a [B, heads, N, d] tensor; sequence b has
+ * n_new[b] <= N tokens in it (n_new NULL: N each) and rows behind them are
+ * padding, neither read into results nor written.
+ *
+ * BSA_CACHE_E4M3 holds one e4m3 code a value and one fp32 scale a token and
+ * key/value head. With amax the largest |x| of the token's d values: scale =
+ * fl32(amax / 448), code = e4m3(fl32(x * fl32(448 / amax))), round to nearest
+ * even; amax < 2^-100 gives scale 1 (and zero codes); a token with a value
+ * that is not finite gets the scale NaN and reads as NaN in every channel.
+ * NaN codes (0x7f, 0xff) are never written, and must not be in the cache.
+ *
+ * Faults found by the kernels, all recorded as BSA_DEVERR_BAD_INDEX: a page
+ * index outside [0, n_pages) where a page is needed (append drops the token,
+ * read gives zeros, the forward reads page 0 in its place), kv_len outside
+ * [0, max_pages * page], n_new outside [0, N], n_new above kv_len for an
+ * append, begin below 0 (clamped; append drops tokens at negative positions).
+ * Slots at or past kv_len[b], and pages that hold no kept token, may hold
+ * anything, NaN included; V of a token below kv_len[b] must be finite unless
+ * every row of the chunk may turn NaN. */
+#define BSA_CACHE_BF16 1
+#define BSA_CACHE_E4M3 2
+
+typedef struct {
+  int32_t kind;            /* BSA_CACHE_BF16 or BSA_CACHE_E4M3                */
+  int32_t n_pages;         /* pages in k and v, >= 1                          */
+  int32_t Hkv;             /* key/value heads                                 */
+  int32_t page;            /* tokens a page: a power of two, 16..1024         */
+  int32_t d;               /* head dimension: 64 or 128                       */
+  int32_t max_pages;       /* row length of table                             */
+  void* k;                 /* device [n_pages, Hkv, page, d], bf16 or uint8   */
+  void* v;                 /* device, as k                                    */
+  float* k_scale;          /* device [n_pages, Hkv, page], e4m3 only          */
+  float* v_scale;          /* device, as k_scale                              */
+  const int32_t* table;    /* device int32 [B, max_pages]                     */
+  const int32_t* kv_len;   /* device int32 [B]                                */
+} bsa_paged_cache;
+
+/* bsa_paged_append: write a chunk's K and V into the cache, at positions
+ * kv_len[b] - n_new[b] .. kv_len[b] - 1.
+ *  dims: B, N and d are read (d equal to the cache's).
+ *  K, V: device bf16 [B, Hkv, N, d]. n_new: device int32 [B] or NULL.
+ *  Two tokens of one call must not share a slot.
+ *  Errors: INVALID_ARG (null or misaligned pointer, bad dims or cache),
+ *  UNSUPPORTED (d not 64/128, page not a power of two in 16..1024), CUDA. */
+int bsa_paged_append(const bsa_dims* dims, const void* K, const void* V, const int32_t* n_new,
+                     const bsa_paged_cache* cache, void* stream);
+
+/* bsa_paged_read: gather tokens back into contiguous bf16, as bsa_forward,
+ * bsa_quantize_fp8 and bsa_select_topk take them: row i of sequence b
+ * receives token begin[b] + i (e4m3: code * scale, rounded to bf16), or zeros
+ * at or past kv_len[b]. Every row is written.
+ *  dims: B, N (rows) and d are read. begin: device int32 [B], or NULL (0).
+ *  K, V: device bf16 [B, Hkv, N, d].
+ *  Errors: as bsa_paged_append. */
+int bsa_paged_read(const bsa_dims* dims, const bsa_paged_cache* cache, const int32_t* begin, void* K, void* V,
+                   void* stream);
+
+/* Workspace bytes bsa_paged_forward needs for these dims and cache on the
+ * current device: a bound that does not depend on the lengths. 0 for
+ * arguments bsa_paged_forward refuses. */
+size_t bsa_paged_workspace_size(const bsa_dims* dims, const bsa_paged_cache* cache);
+
+/* bsa_paged_forward: attention of a chunk's queries over the cached tokens
+ * (append the chunk first). Query head h reads key/value head h / (H / Hkv).
+ * Row i of sequence b is at position p = kv_len[b] - n_new[b] + i and keeps
+ *  causal = 0: every key j < kv_len[b];
+ *  causal = 1: the keys j <= p, and of these, with window > 0, j > p - window.
+ *  o = softmax(scale * q.k) V over the kept keys, fp32 accumulation, the
+ *  weights rounded to bf16 for the product with V, o rounded to bf16; a row
+ *  that keeps no key gives 0. Rows i >= n_new[b] of O are left as they were.
+ *  dims: B, H, N and d are read. Q, O: device bf16 [B, H, N, d].
+ *  window: 0 for none; needs causal = 1. scale: finite and positive.
+ *  workspace: device, at least bsa_paged_workspace_size bytes, 256-byte
+ *  aligned; contents are scratch. Calls whose kernels may overlap (two
+ *  streams, two graphs) need a workspace each.
+ *  Results do not depend on the other sequences' chunks beyond rounding.
+ *  Errors: INVALID_ARG (null or misaligned pointer, bad dims or cache, H not
+ *  a multiple of Hkv, window or scale), UNSUPPORTED (d, page, more than 2^30
+ *  tokens in a row of the table, B * H * N above 2^31 - 1), WORKSPACE, CUDA. */
+int bsa_paged_forward(const bsa_dims* dims, const void* Q, const int32_t* n_new, const bsa_paged_cache* cache,
+                      int32_t causal, int32_t window, float scale, void* workspace, size_t workspace_bytes,
+                      void* O, void* stream);
+
 /* Length of the tile-order sequence for a raster sequence of n_text text
  * tokens plus the GNA grid: text padded to a multiple of the tile volume,
  * plus every (padded) tile. Host only. */

@@ -18,9 +18,10 @@ select     mean-pooled Q/K block scoring with top-k (lmnt.cn BSA post) and
 attention  masked softmax attention in fp64, per-head modes (full / sparse /
            skip with cached output), bf16 round-to-nearest-even.
 permute    raster <-> tile-order token permutation with padding (GNA).
+paged      the paged key/value cache: append, read-back, e4m3 tokens, attention.
 
 Parity status: every function here is pinned by tests under ``tests/`` that
 do not reuse the function's own formula (brute force, closed forms, library
 routines, invariants), except where a docstring says "parity unpinned".
 """
-from . import masks, select, attention, permute  # noqa: F401
+from . import masks, select, attention, paged, permute  # noqa: F401
