@@ -26,6 +26,8 @@ struct PagedParams {
   int G;                   // query heads a key/value head
   int causal, window;
   float scale_log2;        // scale * log2(e)
+  uint64_t wait_limit_ns;  // failure detection: as in AttnParams
+  int withhold_tile;
 };
 
 // A sequence's chunk and cache lengths, clamped to what the arguments hold.
@@ -73,5 +75,11 @@ __host__ __device__ __forceinline__ long long cache_row(const PagedParams& p, in
 cudaError_t launch_paged_append(const PagedParams& p, cudaStream_t stream);
 cudaError_t launch_paged_read(const PagedParams& p, cudaStream_t stream);
 cudaError_t launch_paged_forward(const PagedParams& p, cudaStream_t stream);
+
+struct PagedWork;
+// The forward for G * N <= 16: k and v map the pages in boxes of one 64-key
+// tile's part of a page; grid = persistent CTAs.
+cudaError_t launch_paged_rows(const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p, const PagedWork& w,
+                              int grid, cudaStream_t stream);
 
 }  // namespace bsa

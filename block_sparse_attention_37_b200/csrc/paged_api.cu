@@ -3,7 +3,7 @@
 #include <cmath>
 #include <cstring>
 
-#include "paged.cuh"
+#include "paged_sched.cuh"
 
 namespace bsa {
 namespace {
@@ -56,6 +56,61 @@ int paged_forward_params(const bsa_dims* dims, const bsa_paged_cache* c, PagedPa
   return BSA_OK;
 }
 
+// The cache's K or V for TMA: 128-byte rows of pages in boxes of a page's part
+// of a `keys`-token tile (a token's row is one or two 64-channel halves, or
+// half a 128-byte row for e4m3 codes at d = 64), 128-byte swizzle.
+int make_page_map(CUtensorMap* m, const PagedParams& p, const void* base, int keys) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return BSA_ERR_CUDA;
+  const int page = 1 << p.page_log2;
+  const int box_tokens = page < keys ? page : keys;
+  const bool half = p.e4m3 && p.d == 64;  // two tokens a 128-byte row
+  const cuuint64_t inner = p.e4m3 ? 128 : p.d, rows = half ? page / 2 : page;
+  const cuuint64_t row_bytes = p.e4m3 ? 128 : (cuuint64_t)p.d * 2;
+  cuuint64_t dims[3] = {inner, rows, (cuuint64_t)p.n_pages * p.Hkv};
+  cuuint64_t strides[2] = {row_bytes, rows * row_bytes};
+  cuuint32_t box[3] = {p.e4m3 ? 128u : 64u, (cuuint32_t)(half ? box_tokens / 2 : box_tokens), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, p.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? BSA_OK : BSA_ERR_CUDA;
+}
+
+// How a forward is cut: rows of an item, keys of a tile, persistent CTAs.
+struct PagedCut {
+  int rows, keys, row_tiles, grid;
+};
+
+PagedCut paged_cut(const PagedParams& p) {
+  PagedCut c;
+  c.rows = 16;
+  c.keys = 64;
+  c.row_tiles = ceil_div((long long)p.G * p.N, c.rows);
+  c.grid = 2 * num_sms();
+  return c;
+}
+
+// The items' tiles fit the arithmetic of the line (paged_sched.cuh).
+bool paged_line_fits(const PagedParams& p, const PagedCut& c) {
+  const double tiles = (double)(((long long)p.max_pages << p.page_log2) / c.keys + 2);
+  return (double)p.B * p.Hkv * c.row_tiles * tiles * c.grid < 4e18 && (long long)p.B * c.row_tiles <= 0x7fffffffll;
+}
+
+struct PagedLayout {
+  size_t split, ml, o, total;
+};
+
+PagedLayout paged_layout(const PagedParams& p, const PagedCut& c) {
+  PagedLayout L;
+  L.split = 0;
+  L.ml = align256((size_t)c.grid * sizeof(SplitItem));
+  L.o = L.ml + align256((size_t)2 * c.grid * c.rows * sizeof(float2));
+  L.total = L.o + (size_t)2 * c.grid * c.rows * p.d * sizeof(float);
+  return L;
+}
+
 }  // namespace
 }  // namespace bsa
 
@@ -89,21 +144,25 @@ int bsa_paged_read(const bsa_dims* dims, const bsa_paged_cache* cache, const int
 
 size_t bsa_paged_workspace_size(const bsa_dims* dims, const bsa_paged_cache* cache) {
   PagedParams p;
-  return paged_forward_params(dims, cache, &p) == BSA_OK ? 256 : 0;
+  if (paged_forward_params(dims, cache, &p) != BSA_OK) return 0;
+  const PagedCut c = paged_cut(p);
+  return paged_line_fits(p, c) ? paged_layout(p, c).total : 0;
 }
 
 int bsa_paged_forward(const bsa_dims* dims, const void* Q, const int32_t* n_new, const bsa_paged_cache* cache,
                       int32_t causal, int32_t window, float scale, void* workspace, size_t workspace_bytes,
                       void* O, void* stream) {
   PagedParams p;
-  const int st = paged_forward_params(dims, cache, &p);
+  int st = paged_forward_params(dims, cache, &p);
   if (st != BSA_OK) return st;
+  const PagedCut c = paged_cut(p);
+  if (!paged_line_fits(p, c)) return BSA_ERR_UNSUPPORTED;
   if (!Q || !O || !aligned16(Q) || !aligned16(O)) return BSA_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return BSA_ERR_INVALID_ARG;
   if (window < 0 || (window > 0 && !causal)) return BSA_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || scale <= 0.f) return BSA_ERR_INVALID_ARG;
-  if (!workspace || workspace_bytes < bsa_paged_workspace_size(dims, cache) ||
-      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+  const PagedLayout L = paged_layout(p, c);
+  if (!workspace || workspace_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return BSA_ERR_WORKSPACE;
   p.Q = static_cast<const __nv_bfloat16*>(Q);
   p.O = static_cast<__nv_bfloat16*>(O);
@@ -111,7 +170,17 @@ int bsa_paged_forward(const bsa_dims* dims, const void* Q, const int32_t* n_new,
   p.causal = causal;
   p.window = window;
   p.scale_log2 = scale * 1.4426950408889634f;
-  return cuda_status(launch_paged_forward(p, static_cast<cudaStream_t>(stream)));
+  p.wait_limit_ns = g_wait_limit_ns.load();
+  p.withhold_tile = g_withheld_tile.load();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((long long)p.G * p.N > c.rows) return cuda_status(launch_paged_forward(p, s));
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const PagedWork w{reinterpret_cast<SplitItem*>(ws + L.split), reinterpret_cast<float2*>(ws + L.ml),
+                    reinterpret_cast<float*>(ws + L.o)};
+  CUtensorMap mk, mv;
+  if ((st = make_page_map(&mk, p, p.k, c.keys)) != BSA_OK) return st;
+  if ((st = make_page_map(&mv, p, p.v, c.keys)) != BSA_OK) return st;
+  return cuda_status(launch_paged_rows(mk, mv, p, w, c.grid, s));
 }
 
 }  // extern "C"
