@@ -6,45 +6,61 @@
 // kernel's task is to keep copies in flight. Persistent CTAs (two an SM) each
 // walk one run of the line of 64-key tiles (paged_sched.cuh); a producer warp
 // keeps a ring of tiles full with TMA, a lane a copy (page tables are read by
-// the lanes that need them), and four warps consume: warp w takes keys 16w ..
-// 16w + 15 of every tile for all rows, with a softmax state of its own, so
-// the warps meet only where an item ends. The products are m16n8k16 warp
-// MMAs: with 16 rows a tcgen05 tile would be filled to an eighth, and at the
-// rate HBM delivers keys (23 bytes a clock and SM) the warp MMAs are busy a
-// fifth of the time. The lines are cut to equal runs, so one long sequence
-// fills the GPU like many short ones.
+// the lanes that need them), and groups of four warps take tiles in turn:
+// warp w of a group has keys 16w .. 16w + 15 of its tiles for all rows, with a
+// softmax state of its own, so the warps meet only where an item ends. The
+// products are m16n8k16 warp MMAs with the keys (S^T = K Q^T) and then the
+// channels (O^T = V^T P^T) as the long side, so eight rows fill them: a
+// tcgen05 tile would be filled to a sixteenth, and at the rate HBM delivers
+// keys (23 bytes a clock and SM) the warp MMAs are busy a fifth of the time.
+// The lines are cut to equal runs, so one long sequence fills the GPU like
+// many short ones.
 //
-// e4m3: codes become bf16 in registers (exact). K's scale multiplies the
-// logit, V's the weight before its rounding to bf16, so neither adds an error.
+// e4m3: codes become fp16 in registers (exact). K's scale multiplies the
+// logit; V's, over sigma, the weight: sigma is a power of two, the largest V
+// scale the warp has met, so the weights stay in fp16's range, and O carries
+// 1 / sigma as it carries the running maximum. Weights are held times 2^12:
+// what fp16 flushes is below 2^-36 of the largest, and 11 bits of weight
+// round less than bf16's eight.
 #include "paged_sched.cuh"
 #include "tiles.cuh"
 
+#include <cuda_fp16.h>
+
 namespace bsa {
 
-constexpr int kRowsTile = 16;    // query rows of an item
-constexpr int kRowsKeys = 64;    // keys of a tile
-constexpr int kRowsThreads = 160;
+constexpr int kRowsTile = 16;     // query rows of an item
+constexpr int kRowsKeys = 64;     // keys of a tile
 constexpr int kRowsMinTiles = 2;  // a run is at least this many tiles
+constexpr float kRowsTau = 3.f;   // the state moves when a row's maximum grows by more than 2^3
+constexpr float kRowsGain = 4096.f;  // e4m3: weights (at most 2^3) are held times this in fp16
 
-template <int D, bool E4M3>
+// R8: query rows in eights. NG: groups of four consumer warps.
+template <int D, bool E4M3, int R8, int NG>
 struct RowsCfg {
+  static constexpr int WARPS = 4 * NG;
+  static constexpr int THREADS = 32 * WARPS + 32;
   static constexpr int TOKEN = D * (E4M3 ? 1 : 2);         // bytes of a token's K
   static constexpr int KBYTES = kRowsKeys * TOKEN;
   static constexpr int SCALES = E4M3 ? kRowsKeys * 4 : 0;  // bytes of K's scales
   static constexpr int STAGE = 2 * KBYTES + (E4M3 ? 1024 : 0);  // K, V, scales (1024-aligned stages)
-  // as many stages as two CTAs an SM have room for, at most 8
-  static constexpr int FIT = (100 * 1024) / STAGE;
-  static constexpr int STAGES = FIT > 8 ? 8 : FIT;
-  static constexpr int XCH_OFF = STAGES * STAGE;           // exchange of the warps' outputs: a quarter each
-  static constexpr int ML_OFF = XCH_OFF + kRowsTile * D * 4;
-  static constexpr int BAR_OFF = ML_OFF + 2 * 4 * kRowsTile * 4;
+  // as many stages as two CTAs an SM have room for, at most 8. A multiple of
+  // the groups: every stage then belongs to one group, which sees each of its
+  // phases. With a stage passed from group to group, one could wait for a
+  // phase while the other's tile is still in flight and take the phase before
+  // (same parity) for it.
+  static constexpr int FIT = (104 * 1024) / STAGE;
+  static constexpr int STAGES = (FIT > 8 ? 8 : FIT) / NG * NG;
+  static constexpr int TPR = 2;                            // 16-channel tiles of O joined a round
+  static constexpr int XCH_OFF = STAGES * STAGE;
+  static constexpr int ML_OFF = XCH_OFF + WARPS * TPR * R8 * 512;
+  static constexpr int BAR_OFF = ML_OFF + 2 * WARPS * 8 * R8 * 4;
   static constexpr int MISC_OFF = BAR_OFF + 2 * STAGES * 8;
-  static constexpr int SMEM = MISC_OFF + 16 + sizeof(Run) + 8 * 8;
+  static constexpr int SMEM = MISC_OFF + 16 + sizeof(Run) + 16 * 8;
   static constexpr int ALLOC = SMEM + 1024;
+  static_assert(ALLOC <= 113 * 1024, "two CTAs an SM");
+  static_assert(STAGES >= 2 && STAGES % NG == 0, "a stage belongs to one group");
 };
-static_assert(RowsCfg<128, false>::ALLOC <= 113 * 1024 && RowsCfg<64, false>::ALLOC <= 113 * 1024 &&
-                  RowsCfg<128, true>::ALLOC <= 113 * 1024 && RowsCfg<64, true>::ALLOC <= 113 * 1024,
-              "two CTAs an SM");
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -64,25 +80,54 @@ __device__ __forceinline__ void lds128(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// 8 x 8 16-bit matrix over the warp, transposed
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
-__device__ __forceinline__ uint32_t bits(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t*>(&x); }
-// Bytes 0 and 2, and bytes 1 and 3, of four codes as bf16 pairs.
-__device__ __forceinline__ uint32_t codes_even(uint32_t w) { return bits(e4m3_pair(w << 8, w << 4)); }
-__device__ __forceinline__ uint32_t codes_odd(uint32_t w) { return bits(e4m3_pair(w, w >> 4)); }
+template <bool HALF>
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  if constexpr (HALF)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Two e4m3 codes as an fp16 pair, from the low and the high half of w.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
+  uint32_t y;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(y) : "r"(w));
+  return y;
+}
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
+  uint32_t y;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n\t}" : "=r"(y) : "r"(w));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 
-__device__ __forceinline__ void rows_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void rows_bar() {
+  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kRowsThreads, 2)
+template <int D, bool E4M3, int R8, int NG>
+__global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const PagedParams p, const PagedWork wk) {
-  using C = RowsCfg<D, E4M3>;
-  constexpr int S = C::STAGES;
+  using C = RowsCfg<D, E4M3, R8, NG>;
+  constexpr int S = C::STAGES, W = C::WARPS;
+  constexpr int NR = 2 * R8;  // rows a thread holds: 2t, 2t + 1 of each eight
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
@@ -105,9 +150,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     tma_prefetch_desc(&tmV);
   }
   // (the barriers are published by find_run's own block barriers)
-  Run run = find_run<kRowsTile, kRowsKeys, kRowsThreads>(p, 1, kRowsMinTiles, run_sh, scan_sh);
+  Run run = find_run<kRowsTile, kRowsKeys, C::THREADS>(p, 1, kRowsMinTiles, run_sh, scan_sh);
 
-  if (warp == 4) {
+  if (warp == W) {
     // ------------------------------------------------------------- producer
     const int per = min(1 << p.page_log2, kRowsKeys);  // tokens a copy covers: a page, or a tile of a long page
     const int sub = kRowsKeys / per;
@@ -162,283 +207,364 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
   }
 
   // --------------------------------------------------------------- consumers
-  const int g = lane >> 2, t4 = lane & 3;
+  const int g = lane >> 2, t4 = lane & 3, w4 = warp & 3, grp = warp >> 2;
   const uint32_t sbase = smem_u32(smem);
-  float* xch = reinterpret_cast<float*>(smem + C::XCH_OFF);
   float* sm_m = reinterpret_cast<float*>(smem + C::ML_OFF);
-  float* sm_l = sm_m + 4 * kRowsTile;
+  float* sm_l = sm_m + W * 8 * R8;
   const int rows = p.G * p.N;
-  int k = 0;
+  int k = 0;  // tiles of the run before this piece
   SplitItem split{0, 0, 0, 0};
   while (run.left > 0) {
     const long long at = run.pos;
     const Piece q = next_piece<kRowsTile, kRowsKeys>(p, 1, run);
     if (q.t == 0 && q.m < q.s.nt)
       split = SplitItem{q.b, q.hk, run_of(run.total, at + q.s.nt - 1, run.ctas) - cta + 1, 0};
-    // the rows of this thread: g and g + 8
     const size_t row_base = (size_t)(q.b * p.Hkv + q.hk) * rows;
-    int lo[2], hi[2];
-    bool written[2];
+    // this thread's rows of S^T and O^T: 2t, 2t + 1 of each eight
+    int lo[NR], hi[NR];
+    bool written[NR];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = g + 8 * i;
+    for (int i = 0; i < NR; ++i) {
+      const int r = 8 * (i >> 1) + 2 * t4 + (i & 1);
       const int tok = r < rows ? r - fdiv(r, p.f_n) * p.N : 0;
       written[i] = r < rows && tok < q.n;
       row_keys(p, q.n, q.kv, tok, lo[i], hi[i]);
     }
-    // Q as A fragments. bf16: k-step s covers channels 16 s .. 16 s + 15 in
-    // order. e4m3: the order of the channels inside the steps is the one in
-    // which a lane's 16-byte reads of K deliver them (see below); a dot
-    // product does not mind.
-    uint32_t qf[D / 16][4];
+    // Q as B fragments, row g of each eight. bf16: k-step s covers channels
+    // 16 s .. 16 s + 15 in order. e4m3: fp16 after a power-of-two scale of
+    // the row (exact down to 2^-24 of its largest value), in the order in
+    // which a lane's 16-byte reads of K deliver the channels (see below).
+    uint32_t qf[R8][D / 16][2];
+    float zs[NR];  // row factor of the logits
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s)
+    for (int e = 0; e < R8; ++e) {
+      const int r = 8 * e + g;
+      const int tok = r < rows ? r - fdiv(r, p.f_n) * p.N : 0;
+      const bool have = r < rows && tok < q.n;
+      const __nv_bfloat16* src = p.Q + (row_base + r) * D;
+      if constexpr (E4M3) {
+        uint2 x[D / 16];
+        uint32_t top = 0u;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const __nv_bfloat16* src = p.Q + (row_base + g + 8 * i) * D;
-        if constexpr (E4M3) {
-          uint2 x = make_uint2(0u, 0u);
-          if (written[i]) x = __ldg(reinterpret_cast<const uint2*>(src + 64 * (s >> 2) + 16 * t4 + 4 * (s & 3)));
-          qf[s][i] = __byte_perm(x.x, x.y, 0x5410);
-          qf[s][2 + i] = __byte_perm(x.x, x.y, 0x7632);
-        } else {
-          qf[s][i] = written[i] ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * t4)) : 0u;
-          qf[s][2 + i] = written[i] ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 8 + 2 * t4)) : 0u;
+        for (int s = 0; s < D / 16; ++s) {
+          x[s] = make_uint2(0u, 0u);
+          if (have) x[s] = __ldg(reinterpret_cast<const uint2*>(src + 64 * (s >> 2) + 16 * t4 + 4 * (s & 3)));
+          const uint32_t u = __vmaxu2(x[s].x & 0x7fff7fffu, x[s].y & 0x7fff7fffu);
+          top = max(top, max(u & 0xffffu, u >> 16));
         }
-      }
-    float o[D / 8][4];
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^-e with e the exponent of the largest value, inside the normal range
+        const int ex = min(max((int)(top >> 7), 1), 253);
+        const float down = __int_as_float((254 - ex) << 23), up = __int_as_float(ex << 23);
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
+        for (int s = 0; s < D / 16; ++s) {
+          qf[e][s][0] = pack_f16x2(__uint_as_float(x[s].x << 16) * down, __uint_as_float(x[s].x & 0xffff0000u) * down);
+          qf[e][s][1] = pack_f16x2(__uint_as_float(x[s].y << 16) * down, __uint_as_float(x[s].y & 0xffff0000u) * down);
+        }
+        // rows 2t and 2t + 1 are held by the lanes 8t and 8t + 4
+        zs[2 * e] = __shfl_sync(0xffffffffu, up, 8 * t4) * p.scale_log2;
+        zs[2 * e + 1] = __shfl_sync(0xffffffffu, up, 8 * t4 + 4) * p.scale_log2;
+      } else {
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          qf[e][s][0] = have ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * t4)) : 0u;
+          qf[e][s][1] = have ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 8 + 2 * t4)) : 0u;
+        }
+        zs[2 * e] = zs[2 * e + 1] = p.scale_log2;
+      }
+    }
+    float o[R8][D / 16][4];
+#pragma unroll
+    for (int e = 0; e < R8; ++e)
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) o[e][i][0] = o[e][i][1] = o[e][i][2] = o[e][i][3] = 0.f;
+    float m[NR], l[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      m[i] = kNegInf;
+      l[i] = 0.f;
+    }
+    float sigma = 0x1p-112f;  // e4m3: a power of two, at least every V scale so far
 
-    for (int it = 0; it < q.m; ++it, ++k) {
-      const int st = k % S;
+    // the group's tiles: every NG-th of the run
+    for (int it = (grp + NG - k % NG) % NG; it < q.m; it += NG) {
+      const int st = (k + it) % S;
       const int key0 = (q.s.t0 + q.t + it) * kRowsKeys;
       const bool edge = key0 < q.s.clo || key0 + kRowsKeys > q.s.chi;
-      if (!warp_all(mbar_wait(&full[st], (uint32_t)(k / S) & 1u, abort_flag, p.wait_limit_ns))) {
+      if (!warp_all(mbar_wait(&full[st], (uint32_t)((k + it) / S) & 1u, abort_flag, p.wait_limit_ns))) {
         // every warp sees the flag in its next wait; all go on to the same
         // block barriers, so none is left behind in one (the output is void)
         cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
-        k += q.m - it;
         break;
       }
       const uint32_t kb = sbase + st * C::STAGE, vb = kb + C::KBYTES;
-      // S[16 rows][16 keys]: two n-tiles of eight keys
-      float s2[2][4];
+      // S^T[16 keys][rows]
+      float s2[R8][4];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        s2[nt][0] = s2[nt][1] = s2[nt][2] = s2[nt][3] = 0.f;
-        if constexpr (E4M3) {
-          // lane (key g, t) reads bytes 16 t .. 16 t + 15 of each 64-byte half:
-          // word s of it is k-step s's four values, even bytes then odd bytes
-          const int key = 16 * warp + 8 * nt + g;
+      for (int e = 0; e < R8; ++e) s2[e][0] = s2[e][1] = s2[e][2] = s2[e][3] = 0.f;
+      const float* scl = reinterpret_cast<const float*>(smem + st * C::STAGE + 2 * C::KBYTES) + 16 * w4 + g;
+      if constexpr (E4M3) {
+        // lane (key g, t) reads bytes 16 t .. 16 t + 15 of each 64-byte half:
+        // word s of it holds the four channels of k-step s
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h) {
-            const uint32_t lin = key * C::TOKEN + 64 * h + 16 * t4;
-            uint32_t x[4];
-            lds128(x, kb + (lin ^ ((lin >> 3) & 0x70u)));
+        for (int h = 0; h < D / 64; ++h) {
+          const uint32_t l0 = (16 * w4 + g) * C::TOKEN + 64 * h + 16 * t4, l1 = l0 + 8 * C::TOKEN;
+          uint32_t x[4], y[4];
+          lds128(x, kb + (l0 ^ ((l0 >> 3) & 0x70u)));
+          lds128(y, kb + (l1 ^ ((l1 >> 3) & 0x70u)));
 #pragma unroll
-            for (int s = 0; s < 4; ++s) mma16(s2[nt], qf[4 * h + s], codes_even(x[s]), codes_odd(x[s]));
-          }
-          const float2 sk =
-              *reinterpret_cast<const float2*>(smem + st * C::STAGE + 2 * C::KBYTES + (16 * warp + 8 * nt + 2 * t4) * 4);
-          s2[nt][0] *= sk.x;
-          s2[nt][1] *= sk.y;
-          s2[nt][2] *= sk.x;
-          s2[nt][3] *= sk.y;
-        } else {
-          const int key = 16 * warp + 8 * nt + (lane & 7);
+          for (int s = 0; s < 4; ++s) {
+            const uint32_t a0 = codes_lo(x[s]), a1 = codes_lo(y[s]), a2 = codes_hi(x[s]), a3 = codes_hi(y[s]);
 #pragma unroll
-          for (int h = 0; h < D / 32; ++h) {
-            const int u = 4 * h + (lane >> 3);  // 16-byte unit of the row
-            uint32_t x[4];
-            ldsm4(x, kb + (u >> 3) * kRowsKeys * 128 + key * 128 + (((u ^ key) & 7) << 4));
-            mma16(s2[nt], qf[2 * h], x[0], x[1]);
-            mma16(s2[nt], qf[2 * h + 1], x[2], x[3]);
+            for (int e = 0; e < R8; ++e) mma16<true>(s2[e], a0, a1, a2, a3, qf[e][4 * h + s][0], qf[e][4 * h + s][1]);
           }
         }
+        const float k0 = scl[0], k1 = scl[8];
+#pragma unroll
+        for (int e = 0; e < R8; ++e) {
+          s2[e][0] *= k0;
+          s2[e][1] *= k0;
+          s2[e][2] *= k1;
+          s2[e][3] *= k1;
+        }
+      } else {
+        const int key = 16 * w4 + (lane & 15);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const int u = 2 * s + (lane >> 4);  // 16-byte unit of the row
+          uint32_t x[4];
+          ldsm4(x, kb + (u >> 3) * kRowsKeys * 128 + key * 128 + (((u ^ key) & 7) << 4));
+#pragma unroll
+          for (int e = 0; e < R8; ++e) mma16<false>(s2[e], x[0], x[1], x[2], x[3], qf[e][s][0], qf[e][s][1]);
+        }
       }
+      const int j0 = key0 + 16 * w4 + g;  // this thread's keys: j0 and j0 + 8
       if (edge) {
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int e = 0; e < R8; ++e)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int j = key0 + 16 * warp + 8 * nt + 2 * t4 + (c & 1);
-            if (j < lo[c >> 1] || j >= hi[c >> 1]) s2[nt][c] = kNegInf;
+            const int j = j0 + 8 * (c >> 1), i = 2 * e + (c & 1);
+            if (j < lo[i] || j >= hi[i]) s2[e][c] = kNegInf;
           }
       }
-      // online softmax; the state moves only when a row's maximum grows by
-      // more than 2^8 (weights then reach 2^8, within bf16's range)
+      // online softmax; the state moves only when a row's maximum grows by more than 2^kRowsTau
       bool moved = false;
-      float mu[2];
-      float alpha[2];
+      float mu[NR], alpha[NR];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float x = fmaxf(fmaxf(s2[0][2 * i], s2[0][2 * i + 1]), fmaxf(s2[1][2 * i], s2[1][2 * i + 1]));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        x *= p.scale_log2;
+      for (int i = 0; i < NR; ++i) {
+        float x = fmaxf(s2[i >> 1][i & 1], s2[i >> 1][2 + (i & 1)]);
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        x *= zs[i];
         alpha[i] = 1.f;
-        if (x > m[i] + 8.f) {
+        if (x > m[i] + kRowsTau) {
           alpha[i] = fast_exp2(m[i] - x);
           m[i] = x;
           moved = true;
         }
         mu[i] = m[i] == kNegInf ? 0.f : m[i];
       }
+      float rs = 0.f;  // e4m3: gain / sigma
+      float beta = 1.f;
+      float v0 = 0.f, v1 = 0.f;
+      if constexpr (E4M3) {
+        v0 = scl[C::SCALES / 4];
+        v1 = scl[C::SCALES / 4 + 8];
+        if (edge) {  // scales of keys no row keeps may be anything
+          v0 = j0 >= q.s.lo && j0 < q.s.hi ? v0 : 0.f;
+          v1 = j0 + 8 >= q.s.lo && j0 + 8 < q.s.hi ? v1 : 0.f;
+        }
+        // the largest finite scale of the warp's keys, as bits
+        const uint32_t b0 = __float_as_uint(v0), b1 = __float_as_uint(v1);
+        const uint32_t top = __reduce_max_sync(0xffffffffu, max(b0 < 0x7f800000u ? b0 : 0u, b1 < 0x7f800000u ? b1 : 0u));
+        if (top > __float_as_uint(sigma)) {
+          const float up = __uint_as_float(min((top + 0x7fffffu) & 0x7f800000u, 0x7f000000u));
+          beta = sigma / up;
+          sigma = up;
+          moved = true;
+        }
+        rs = kRowsGain / sigma;
+      }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][0] *= alpha[0];
-          o[i][1] *= alpha[0];
-          o[i][2] *= alpha[1];
-          o[i][3] *= alpha[1];
-        }
-        l[0] *= alpha[0];
-        l[1] *= alpha[1];
-      }
+        for (int e = 0; e < R8; ++e)
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+          for (int i = 0; i < D / 16; ++i) {
+            o[e][i][0] *= alpha[2 * e] * beta;
+            o[e][i][1] *= alpha[2 * e + 1] * beta;
+            o[e][i][2] *= alpha[2 * e] * beta;
+            o[e][i][3] *= alpha[2 * e + 1] * beta;
+          }
+#pragma unroll
+        for (int i = 0; i < NR; ++i) l[i] *= alpha[i];
+      }
+      uint32_t pf[R8][2];
+#pragma unroll
+      for (int e = 0; e < R8; ++e) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          s2[nt][c] = fast_exp2(fmaf(s2[nt][c], p.scale_log2, -mu[c >> 1]));
-          l[c >> 1] += s2[nt][c];
+          const int i = 2 * e + (c & 1);
+          s2[e][c] = fast_exp2(fmaf(s2[e][c], zs[i], -mu[i]));
+          l[i] += s2[e][c];
         }
+        if constexpr (E4M3) {
+          const float f0 = v0 * rs, f1 = v1 * rs;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float x = s2[e][c] * (c < 2 ? f0 : f1);
+            s2[e][c] = s2[e][c] == 0.f ? 0.f : x;  // a key of no weight adds nothing, whatever its scale
+          }
+          pf[e][0] = movm(pack_f16x2(s2[e][0], s2[e][1]));
+          pf[e][1] = movm(pack_f16x2(s2[e][2], s2[e][3]));
+        } else {
+          pf[e][0] = movm(pack_bf16x2(s2[e][0], s2[e][1]));
+          pf[e][1] = movm(pack_bf16x2(s2[e][2], s2[e][3]));
+        }
+      }
       uint32_t vm[2] = {0xffffffffu, 0xffffffffu};  // V of keys no row keeps reads as zero
       if (edge) {
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const int j = key0 + 16 * warp + 8 * nt + 2 * t4;
-          if (j < q.s.lo || j >= q.s.hi) vm[nt] &= 0xffff0000u;
-          if (j + 1 < q.s.lo || j + 1 >= q.s.hi) vm[nt] &= 0x0000ffffu;
+        for (int h = 0; h < 2; ++h) {
+          const int j = key0 + 16 * w4 + 8 * h + 2 * t4;
+          if (j < q.s.lo || j >= q.s.hi) vm[h] &= 0xffff0000u;
+          if (j + 1 < q.s.lo || j + 1 >= q.s.hi) vm[h] &= 0x0000ffffu;
         }
       }
+      // O^T += V^T P^T: matrices of eight keys x 16 bytes, transposed on the way in
       if constexpr (E4M3) {
+        // 16-bit columns are channel pairs: channel 2g of a 16-byte unit is
+        // row g of the tile, channel 2g + 1 row g + 8
+        const int vkey = 16 * w4 + (lane & 15);
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          float2 sv = *reinterpret_cast<const float2*>(smem + st * C::STAGE + 2 * C::KBYTES + C::SCALES +
-                                                       (16 * warp + 8 * nt + 2 * t4) * 4);
-          if (edge) {
-            if (!(vm[nt] & 0xffffu)) sv.x = 0.f;
-            if (!(vm[nt] >> 16)) sv.y = 0.f;
-          }
-          s2[nt][0] *= sv.x;
-          s2[nt][1] *= sv.y;
-          s2[nt][2] *= sv.x;
-          s2[nt][3] *= sv.y;
-        }
-      }
-      const uint32_t pf[4] = {pack_bf16x2(s2[0][0], s2[0][1]), pack_bf16x2(s2[0][2], s2[0][3]),
-                              pack_bf16x2(s2[1][0], s2[1][1]), pack_bf16x2(s2[1][2], s2[1][3])};
-      // O += P V: matrices of eight keys x 16 bytes, transposed on the way in
-      const int vkey = 16 * warp + (lane & 15);
-#pragma unroll
-      for (int h = 0; h < C::TOKEN / 32; ++h) {
-        const int u = 2 * h + (lane >> 4);
-        uint32_t x[4];
-        if constexpr (E4M3) {
-          // 16-bit columns are channel pairs: even channels make one n-tile, odd ones the next
-          const uint32_t lin = vkey * C::TOKEN + u * 16;
+        for (int h = 0; h < D / 32; ++h) {
+          const uint32_t lin = vkey * C::TOKEN + (2 * h + (lane >> 4)) * 16;
+          uint32_t x[4];
           ldsm4t(x, vb + (lin ^ ((lin >> 3) & 0x70u)));
-          mma16(o[4 * h], pf, codes_even(x[0]), codes_even(x[1]));
-          mma16(o[4 * h + 1], pf, codes_odd(x[0]), codes_odd(x[1]));
-          mma16(o[4 * h + 2], pf, codes_even(x[2]), codes_even(x[3]));
-          mma16(o[4 * h + 3], pf, codes_odd(x[2]), codes_odd(x[3]));
-        } else {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t y = __byte_perm(x[2 * u], 0u, 0x3120), z = __byte_perm(x[2 * u + 1], 0u, 0x3120);
+            uint32_t a0 = codes_lo(y), a1 = codes_hi(y), a2 = codes_lo(z), a3 = codes_hi(z);
+            if (edge) {
+              a0 &= vm[0];
+              a1 &= vm[0];
+              a2 &= vm[1];
+              a3 &= vm[1];
+            }
+#pragma unroll
+            for (int e = 0; e < R8; ++e) mma16<true>(o[e][2 * h + u], a0, a1, a2, a3, pf[e][0], pf[e][1]);
+          }
+        }
+      } else {
+        const int vkey = 16 * w4 + (lane >> 4) * 8 + (lane & 7);
+#pragma unroll
+        for (int h = 0; h < D / 16; ++h) {
+          const int u = 2 * h + ((lane >> 3) & 1);
+          uint32_t x[4];
           ldsm4t(x, vb + (u >> 3) * kRowsKeys * 128 + vkey * 128 + (((u ^ vkey) & 7) << 4));
           if (edge) {
             x[0] &= vm[0];
-            x[1] &= vm[1];
-            x[2] &= vm[0];
+            x[1] &= vm[0];
+            x[2] &= vm[1];
             x[3] &= vm[1];
           }
-          mma16(o[2 * h], pf, x[0], x[1]);
-          mma16(o[2 * h + 1], pf, x[2], x[3]);
+#pragma unroll
+          for (int e = 0; e < R8; ++e) mma16<false>(o[e][h], x[0], x[1], x[2], x[3], pf[e][0], pf[e][1]);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
     }
+    k += q.m;
 
-    // ------------------------------------------------ join the four warps
+    // ------------------------------------------------ join the warps
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if (t4 == 0) {
-        sm_m[warp * kRowsTile + g + 8 * i] = m[i];
-        sm_l[warp * kRowsTile + g + 8 * i] = l[i];
+    for (int i = 0; i < NR; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 4);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 8);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 16);
+      if (g == 0) {
+        const int at8 = warp * 8 * R8 + 8 * (i >> 1) + 2 * t4 + (i & 1);
+        sm_m[at8] = m[i];
+        sm_l[at8] = l[i];
       }
     }
-    rows_bar();
-    float M[2], L[2], sc[2];
+    rows_bar<32 * W>();
+    float M[NR], L[NR], sc[NR];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NR; ++i) {
+      const int at8 = 8 * (i >> 1) + 2 * t4 + (i & 1);
       M[i] = kNegInf;
       L[i] = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) M[i] = fmaxf(M[i], sm_m[w * kRowsTile + g + 8 * i]);
+      for (int w = 0; w < W; ++w) M[i] = fmaxf(M[i], sm_m[w * 8 * R8 + at8]);
       const float mu = M[i] == kNegInf ? 0.f : M[i];
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
-        L[i] += sm_l[w * kRowsTile + g + 8 * i] * fast_exp2(sm_m[w * kRowsTile + g + 8 * i] - mu);
+      for (int w = 0; w < W; ++w) L[i] += sm_l[w * 8 * R8 + at8] * fast_exp2(sm_m[w * 8 * R8 + at8] - mu);
       sc[i] = fast_exp2(m[i] - mu);
+      if constexpr (E4M3) sc[i] *= sigma * (1.f / kRowsGain);
     }
-    // each warp ends with a quarter of the channels, summed over the warps
-    constexpr int QT = D / 32;  // n-tiles a quarter
-    float own[QT][4];
-    float4* slots = reinterpret_cast<float4*>(xch);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-#pragma unroll
-      for (int i = 0; i < QT; ++i)
-        slots[(warp * QT + i) * 32 + lane] = make_float4(o[w * QT + i][0] * sc[0], o[w * QT + i][1] * sc[0],
-                                                         o[w * QT + i][2] * sc[1], o[w * QT + i][3] * sc[1]);
-      rows_bar();
-      if (w == warp)
-#pragma unroll
-        for (int i = 0; i < QT; ++i) {
-          const float4 x0 = slots[i * 32 + lane], x1 = slots[(QT + i) * 32 + lane];
-          const float4 x2 = slots[(2 * QT + i) * 32 + lane], x3 = slots[(3 * QT + i) * 32 + lane];
-          own[i][0] = (x0.x + x1.x) + (x2.x + x3.x);
-          own[i][1] = (x0.y + x1.y) + (x2.y + x3.y);
-          own[i][2] = (x0.z + x1.z) + (x2.z + x3.z);
-          own[i][3] = (x0.w + x1.w) + (x2.w + x3.w);
-        }
-      rows_bar();
-    }
+    // TPR of O's tiles a round; warp w of the round's tiles sums and stores tile w
     const bool whole = q.whole();
     const size_t slot = 2 * (size_t)cta + (q.t == 0 ? 1 : 0);
+    float4* slots = reinterpret_cast<float4*>(smem + C::XCH_OFF);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (!written[i]) continue;
-      const int r = g + 8 * i;
-      const float inv = !whole ? 1.f : L[i] > 0.f ? 1.f / L[i] : L[i] == 0.f ? 0.f : L[i];
-      float* po = wk.o + (slot * kRowsTile + r) * D;
-      __nv_bfloat16* oo = p.O + (row_base + r) * D;
-      if constexpr (E4M3) {
+    for (int rd = 0; rd < D / 16 / C::TPR; ++rd) {
 #pragma unroll
-        for (int h = 0; h < QT / 2; ++h) {
-          const int d = 16 * (warp * QT / 2 + h) + 4 * t4;
-          const float4 x = make_float4(own[2 * h][2 * i] * inv, own[2 * h + 1][2 * i] * inv,
-                                       own[2 * h][2 * i + 1] * inv, own[2 * h + 1][2 * i + 1] * inv);
-          if (whole)
-            *reinterpret_cast<uint2*>(oo + d) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-          else
-            *reinterpret_cast<float4*>(po + d) = x;
+      for (int u = 0; u < C::TPR; ++u)
+#pragma unroll
+        for (int e = 0; e < R8; ++e) {
+          const float(&x)[4] = o[e][rd * C::TPR + u];
+          slots[((warp * C::TPR + u) * R8 + e) * 32 + lane] =
+              make_float4(x[0] * sc[2 * e], x[1] * sc[2 * e + 1], x[2] * sc[2 * e], x[3] * sc[2 * e + 1]);
         }
-      } else {
+      rows_bar<32 * W>();
+      // (tile u, eight e) of the round by one warp
+      if (warp < C::TPR * R8) {
+        const int u = warp / R8, e = warp % R8;
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int h = 0; h < QT; ++h) {
-          const int d = 8 * (warp * QT + h) + 2 * t4;
-          const float a = own[h][2 * i] * inv, b = own[h][2 * i + 1] * inv;
-          if (whole)
-            *reinterpret_cast<uint32_t*>(oo + d) = pack_bf16x2(a, b);
-          else
-            *reinterpret_cast<float2*>(po + d) = make_float2(a, b);
+        for (int w = 0; w < W; ++w) {
+          const float4 x = slots[((w * C::TPR + u) * R8 + e) * 32 + lane];
+          acc[0] += x.x;
+          acc[1] += x.y;
+          acc[2] += x.z;
+          acc[3] += x.w;
+        }
+        const int t16 = rd * C::TPR + u;
+        const int d0 = 16 * t16 + (E4M3 ? 2 * g : g), d1 = d0 + (E4M3 ? 1 : 8);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int r = 8 * e + 2 * t4 + c;
+          // this row's sums are held under index 2 e + c
+          float Lr = L[c], Mr = M[c];
+          bool wr = written[c];
+          if (R8 == 2 && e == 1) {
+            Lr = L[NR - 2 + c];
+            Mr = M[NR - 2 + c];
+            wr = written[NR - 2 + c];
+          }
+          if (!wr) continue;
+          if (whole) {
+            const float inv = Lr > 0.f ? 1.f / Lr : Lr == 0.f ? 0.f : Lr;
+            __nv_bfloat16* dst = p.O + (row_base + r) * D;
+            if constexpr (E4M3) {
+              *reinterpret_cast<uint32_t*>(dst + d0) = pack_bf16x2(acc[c] * inv, acc[2 + c] * inv);
+            } else {
+              dst[d0] = __float2bfloat16(acc[c] * inv);
+              dst[d1] = __float2bfloat16(acc[2 + c] * inv);
+            }
+          } else {
+            float* dst = wk.o + (slot * kRowsTile + r) * D;
+            dst[d0] = acc[c];
+            dst[d1] = acc[2 + c];
+            if (rd == 0 && u == 0 && g == 0) wk.ml[slot * kRowsTile + r] = make_float2(Mr, Lr);
+          }
         }
       }
-      if (!whole && warp == 0 && t4 == 0) wk.ml[slot * kRowsTile + r] = make_float2(M[i], L[i]);
+      rows_bar<32 * W>();
     }
   }
   if (tid == 0) wk.split[cta] = split;
@@ -514,28 +640,39 @@ static cudaError_t launch_after(K kernel, dim3 grid, unsigned block, cudaStream_
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int R8, int NG>
 static cudaError_t launch_rows_d(const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p, const PagedWork& w,
                                  int grid, cudaStream_t stream) {
-  using C = RowsCfg<D, E4M3>;
-  auto fn = paged_rows_kernel<D, E4M3>;
+  using C = RowsCfg<D, E4M3, R8, NG>;
+  auto fn = paged_rows_kernel<D, E4M3, R8, NG>;
   static DeviceOnce once;
   cudaError_t e = once.run(
       [&]() -> cudaError_t { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC); });
   if (e != cudaSuccess) return e;
-  fn<<<grid, kRowsThreads, C::ALLOC, stream>>>(k, v, p, w);
+  fn<<<grid, C::THREADS, C::ALLOC, stream>>>(k, v, p, w);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int rows = p.G * p.N;
   return launch_after(paged_join_kernel<D, kRowsTile>, dim3(grid, min(rows, 8)), 256, stream, p, w, 1);
 }
 
+template <int D, bool E4M3>
+static cudaError_t launch_rows_any(const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p,
+                                   const PagedWork& w, int grid, cudaStream_t stream) {
+  // Up to eight rows leave the registers for a second group of warps, which
+  // the conversion of e4m3 codes needs; bf16 at d = 128 has three stages' room
+  // and one group keeps up with HBM.
+  constexpr int NG = E4M3 || D == 64 ? 2 : 1;
+  if (p.G * p.N <= 8) return launch_rows_d<D, E4M3, 1, NG>(k, v, p, w, grid, stream);
+  return launch_rows_d<D, E4M3, 2, 1>(k, v, p, w, grid, stream);
+}
+
 cudaError_t launch_paged_rows(const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p, const PagedWork& w,
                               int grid, cudaStream_t stream) {
   if (p.d == 64)
-    return p.e4m3 ? launch_rows_d<64, true>(k, v, p, w, grid, stream)
-                  : launch_rows_d<64, false>(k, v, p, w, grid, stream);
-  return p.e4m3 ? launch_rows_d<128, true>(k, v, p, w, grid, stream)
-                : launch_rows_d<128, false>(k, v, p, w, grid, stream);
+    return p.e4m3 ? launch_rows_any<64, true>(k, v, p, w, grid, stream)
+                  : launch_rows_any<64, false>(k, v, p, w, grid, stream);
+  return p.e4m3 ? launch_rows_any<128, true>(k, v, p, w, grid, stream)
+                : launch_rows_any<128, false>(k, v, p, w, grid, stream);
 }
 
 }  // namespace bsa
