@@ -209,6 +209,19 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
   // --------------------------------------------------------------- consumers
   const int g = lane >> 2, t4 = lane & 3, w4 = warp & 3, grp = warp >> 2;
   const uint32_t sbase = smem_u32(smem);
+  // where this lane's first reads of a tile's K and V lie (128-byte swizzle:
+  // 16-byte unit u of 128-byte row r sits at u ^ (r & 7)); the tile starts on
+  // 1024 bytes, so the further units of a row are an XOR away
+  uint32_t k_off, v_off;
+  if constexpr (E4M3) {
+    const uint32_t kl = (16 * w4 + g) * C::TOKEN + 16 * t4, vl = (16 * w4 + (lane & 15)) * C::TOKEN + (lane >> 4) * 16;
+    k_off = kl ^ ((kl >> 3) & 0x70u);
+    v_off = vl ^ ((vl >> 3) & 0x70u);
+  } else {
+    const uint32_t kk = 16 * w4 + (lane & 15), vk = 16 * w4 + (lane >> 4) * 8 + (lane & 7);
+    k_off = kk * 128 + (((lane >> 4) ^ (kk & 7)) << 4);
+    v_off = vk * 128 + ((((lane >> 3) & 1) ^ (vk & 7)) << 4);
+  }
   float* sm_m = reinterpret_cast<float*>(smem + C::ML_OFF);
   float* sm_l = sm_m + W * 8 * R8;
   const int rows = p.G * p.N;
@@ -279,13 +292,14 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
     for (int e = 0; e < R8; ++e)
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) o[e][i][0] = o[e][i][1] = o[e][i][2] = o[e][i][3] = 0.f;
-    float m[NR], l[NR];
+    float m[NR], mu[NR], l[NR];  // running maximum (log2 units), the same or 0 before there is one, sum
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
       m[i] = kNegInf;
-      l[i] = 0.f;
+      mu[i] = l[i] = 0.f;
     }
-    float sigma = 0x1p-112f;  // e4m3: a power of two, at least every V scale so far
+    // e4m3: a power of two, at least every finite V scale so far, and gain / sigma
+    float sigma = 0x1p-112f, rs = kRowsGain / 0x1p-112f;
 
     // the group's tiles: every NG-th of the run
     for (int it = (grp + NG - k % NG) % NG; it < q.m; it += NG) {
@@ -309,10 +323,9 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
         // word s of it holds the four channels of k-step s
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
-          const uint32_t l0 = (16 * w4 + g) * C::TOKEN + 64 * h + 16 * t4, l1 = l0 + 8 * C::TOKEN;
           uint32_t x[4], y[4];
-          lds128(x, kb + (l0 ^ ((l0 >> 3) & 0x70u)));
-          lds128(y, kb + (l1 ^ ((l1 >> 3) & 0x70u)));
+          lds128(x, (kb + k_off) ^ (64 * h));
+          lds128(y, D == 64 ? (kb + k_off + 512) ^ 64 : (kb + k_off + 1024) ^ (64 * h));
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
             const uint32_t a0 = codes_lo(x[s]), a1 = codes_lo(y[s]), a2 = codes_hi(x[s]), a3 = codes_hi(y[s]);
@@ -329,12 +342,10 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
           s2[e][3] *= k1;
         }
       } else {
-        const int key = 16 * w4 + (lane & 15);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
-          const int u = 2 * s + (lane >> 4);  // 16-byte unit of the row
           uint32_t x[4];
-          ldsm4(x, kb + (u >> 3) * kRowsKeys * 128 + key * 128 + (((u ^ key) & 7) << 4));
+          ldsm4(x, (kb + (s >> 2) * kRowsKeys * 128 + k_off) ^ (32 * (s & 3)));
 #pragma unroll
           for (int e = 0; e < R8; ++e) mma16<false>(s2[e], x[0], x[1], x[2], x[3], qf[e][s][0], qf[e][s][1]);
         }
@@ -349,26 +360,13 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
             if (j < lo[i] || j >= hi[i]) s2[e][c] = kNegInf;
           }
       }
-      // online softmax; the state moves only when a row's maximum grows by more than 2^kRowsTau
-      bool moved = false;
-      float mu[NR], alpha[NR];
+      // online softmax; the state moves only when a row's maximum grows by
+      // more than 2^kRowsTau (or a V scale passes sigma), which a vote finds
+      // without the maximum itself
+      bool over = false;
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        float x = fmaxf(s2[i >> 1][i & 1], s2[i >> 1][2 + (i & 1)]);
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-        x *= zs[i];
-        alpha[i] = 1.f;
-        if (x > m[i] + kRowsTau) {
-          alpha[i] = fast_exp2(m[i] - x);
-          m[i] = x;
-          moved = true;
-        }
-        mu[i] = m[i] == kNegInf ? 0.f : m[i];
-      }
-      float rs = 0.f;  // e4m3: gain / sigma
-      float beta = 1.f;
+      for (int i = 0; i < NR; ++i)
+        over |= fmaxf(s2[i >> 1][i & 1], s2[i >> 1][2 + (i & 1)]) * zs[i] > m[i] + kRowsTau;
       float v0 = 0.f, v1 = 0.f;
       if constexpr (E4M3) {
         v0 = scl[C::SCALES / 4];
@@ -377,29 +375,49 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
           v0 = j0 >= q.s.lo && j0 < q.s.hi ? v0 : 0.f;
           v1 = j0 + 8 >= q.s.lo && j0 + 8 < q.s.hi ? v1 : 0.f;
         }
-        // the largest finite scale of the warp's keys, as bits
-        const uint32_t b0 = __float_as_uint(v0), b1 = __float_as_uint(v1);
-        const uint32_t top = __reduce_max_sync(0xffffffffu, max(b0 < 0x7f800000u ? b0 : 0u, b1 < 0x7f800000u ? b1 : 0u));
-        if (top > __float_as_uint(sigma)) {
-          const float up = __uint_as_float(min((top + 0x7fffffu) & 0x7f800000u, 0x7f000000u));
-          beta = sigma / up;
-          sigma = up;
-          moved = true;
-        }
-        rs = kRowsGain / sigma;
+        over |= fmaxf(v0, v1) > sigma;
       }
-      if (__any_sync(0xffffffffu, moved)) {
+      if (__any_sync(0xffffffffu, over)) {
+        float alpha[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          float x = fmaxf(s2[i >> 1][i & 1], s2[i >> 1][2 + (i & 1)]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          x *= zs[i];
+          alpha[i] = 1.f;
+          if (x > m[i] + kRowsTau) {
+            alpha[i] = fast_exp2(m[i] - x);
+            m[i] = x;
+          }
+          l[i] *= alpha[i];
+        }
+        if constexpr (E4M3) {
+          // the largest finite scale of the warp's keys, as bits
+          const uint32_t b0 = __float_as_uint(v0), b1 = __float_as_uint(v1);
+          const uint32_t top =
+              __reduce_max_sync(0xffffffffu, max(b0 < 0x7f800000u ? b0 : 0u, b1 < 0x7f800000u ? b1 : 0u));
+          if (top > __float_as_uint(sigma)) {
+            const float up = __uint_as_float(min((top + 0x7fffffu) & 0x7f800000u, 0x7f000000u));
+            const float beta = sigma / up;
+            sigma = up;
+            rs = kRowsGain / sigma;
+#pragma unroll
+            for (int i = 0; i < NR; ++i) alpha[i] *= beta;
+          }
+        }
 #pragma unroll
         for (int e = 0; e < R8; ++e)
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
-            o[e][i][0] *= alpha[2 * e] * beta;
-            o[e][i][1] *= alpha[2 * e + 1] * beta;
-            o[e][i][2] *= alpha[2 * e] * beta;
-            o[e][i][3] *= alpha[2 * e + 1] * beta;
+            o[e][i][0] *= alpha[2 * e];
+            o[e][i][1] *= alpha[2 * e + 1];
+            o[e][i][2] *= alpha[2 * e];
+            o[e][i][3] *= alpha[2 * e + 1];
           }
 #pragma unroll
-        for (int i = 0; i < NR; ++i) l[i] *= alpha[i];
+        for (int i = 0; i < NR; ++i) mu[i] = m[i] == kNegInf ? 0.f : m[i];
       }
       uint32_t pf[R8][2];
 #pragma unroll
@@ -415,7 +433,8 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const float x = s2[e][c] * (c < 2 ? f0 : f1);
-            s2[e][c] = s2[e][c] == 0.f ? 0.f : x;  // a key of no weight adds nothing, whatever its scale
+            // a masked key adds nothing, whatever its scale
+            s2[e][c] = edge && s2[e][c] == 0.f ? 0.f : x;
           }
           pf[e][0] = movm(pack_f16x2(s2[e][0], s2[e][1]));
           pf[e][1] = movm(pack_f16x2(s2[e][2], s2[e][3]));
@@ -437,12 +456,10 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
       if constexpr (E4M3) {
         // 16-bit columns are channel pairs: channel 2g of a 16-byte unit is
         // row g of the tile, channel 2g + 1 row g + 8
-        const int vkey = 16 * w4 + (lane & 15);
 #pragma unroll
         for (int h = 0; h < D / 32; ++h) {
-          const uint32_t lin = vkey * C::TOKEN + (2 * h + (lane >> 4)) * 16;
           uint32_t x[4];
-          ldsm4t(x, vb + (lin ^ ((lin >> 3) & 0x70u)));
+          ldsm4t(x, (vb + v_off) ^ (32 * h));
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const uint32_t y = __byte_perm(x[2 * u], 0u, 0x3120), z = __byte_perm(x[2 * u + 1], 0u, 0x3120);
@@ -458,12 +475,10 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
           }
         }
       } else {
-        const int vkey = 16 * w4 + (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
         for (int h = 0; h < D / 16; ++h) {
-          const int u = 2 * h + ((lane >> 3) & 1);
           uint32_t x[4];
-          ldsm4t(x, vb + (u >> 3) * kRowsKeys * 128 + vkey * 128 + (((u ^ vkey) & 7) << 4));
+          ldsm4t(x, (vb + (h >> 2) * kRowsKeys * 128 + v_off) ^ (32 * (h & 3)));
           if (edge) {
             x[0] &= vm[0];
             x[1] &= vm[0];
