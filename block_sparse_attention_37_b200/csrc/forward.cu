@@ -23,10 +23,9 @@
 // FlashAttention tiles with online softmax over the selected blocks;
 // DiTFastAttnV2 "Fused Kernel").
 // Output leaves through shared memory and a TMA store.
-#include <utility>
-
 #include <type_traits>
 
+#include "mma_steps.cuh"
 #include "tiles.cuh"
 
 namespace bsa {
@@ -99,19 +98,6 @@ __device__ __forceinline__ bool gna_on(const AttnParams& p) {
 template <int MK>
 __device__ __forceinline__ bool gna_slice(const AttnParams& p) {
   return MK == kMaskGnaSlice || (p.has_gna && p.g.seg_one_slice);
-}
-
-template <int N>
-__device__ __forceinline__ void regs_release() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_claim() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-__device__ __forceinline__ void named_bar(int id, int n) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* src, int c0, int c1, int c2) {
@@ -381,32 +367,6 @@ __device__ void reorder_tiles(int32_t* sched, int32_t* tmp, int n, int act, int 
   __syncwarp();
   for (int i = lane; i < 2 * full; i += 32) sched[i] = tmp[i];
   __syncwarp();
-}
-
-// S = Q K^T over D/16 k-steps of 16 (K-major SW128 operands: k-step kk sits
-// in 64-column chunk kk/4 (16 KB apart) at byte offset 32*(kk%4)).
-template <int KK>
-__device__ __forceinline__ void qk_step(uint32_t s_tmem, uint64_t qd, uint64_t kd, uint32_t idesc) {
-  constexpr uint32_t off = ((KK >> 2) * 16384 + (KK & 3) * 32) >> 4;
-  umma_ss_at_warp<off, off>(s_tmem, qd, kd, idesc, KK > 0 ? 1u : 0u);
-}
-template <int... KK>
-__device__ __forceinline__ void qk_all(uint32_t s_tmem, uint64_t qd, uint64_t kd, uint32_t idesc,
-                                       std::integer_sequence<int, KK...>) {
-  (qk_step<KK>(s_tmem, qd, kd, idesc), ...);
-}
-
-// O (+)= P V over 8 k-steps of 16 keys: P from tensor memory (8 columns per
-// step), V MN-major SW128 (16 rows = 2048 bytes per step).
-template <int KK>
-__device__ __forceinline__ void pv_step(uint32_t o_tmem, uint32_t p_tmem, uint64_t vd, uint32_t idesc, uint32_t first) {
-  constexpr uint32_t voff = KK * 2048 / 16;
-  umma_ts_at_warp<KK * 8, voff>(o_tmem, p_tmem, vd, idesc, (KK > 0 || !first) ? 1u : 0u);
-}
-template <int... KK>
-__device__ __forceinline__ void pv_all(uint32_t o_tmem, uint32_t p_tmem, uint64_t vd, uint32_t idesc, uint32_t first,
-                                       std::integer_sequence<int, KK...>) {
-  (pv_step<KK>(o_tmem, p_tmem, vd, idesc, first), ...);
 }
 
 // e4m3: S = Q K^T over 4 k-steps of 32 values (32 bytes of the one 128-byte

@@ -74,12 +74,14 @@ __host__ __device__ __forceinline__ long long cache_row(const PagedParams& p, in
 
 cudaError_t launch_paged_append(const PagedParams& p, cudaStream_t stream);
 cudaError_t launch_paged_read(const PagedParams& p, cudaStream_t stream);
-cudaError_t launch_paged_forward(const PagedParams& p, cudaStream_t stream);
-
 struct PagedWork;
 // The forward for G * N <= 16: k and v map the pages in boxes of one 64-key
 // tile's part of a page; grid = persistent CTAs.
 cudaError_t launch_paged_rows(const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p, const PagedWork& w,
                               int grid, cudaStream_t stream);
+// The forward for more rows: items of `rows` (128 or 256) packed rows, q maps
+// [B * Hkv, G * N, d].
+cudaError_t launch_paged_tiles(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p,
+                               const PagedWork& w, int rows, int row_tiles, int grid, cudaStream_t stream);
 
 }  // namespace bsa

@@ -84,11 +84,14 @@ struct PagedCut {
 };
 
 PagedCut paged_cut(const PagedParams& p) {
+  // Up to 16 rows a key/value head the warp MMAs keep up with HBM; more rows
+  // need the tensor core's tiles, 128 rows or 256 an item.
+  const long long rows = (long long)p.G * p.N;
   PagedCut c;
-  c.rows = 16;
-  c.keys = 64;
-  c.row_tiles = ceil_div((long long)p.G * p.N, c.rows);
-  c.grid = 2 * num_sms();
+  c.rows = rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
+  c.keys = c.rows == 16 ? 64 : 128;  // tile of the line (e4m3 codes are copied 64 keys at a time)
+  c.row_tiles = ceil_div(rows, c.rows);
+  c.grid = (c.rows == 16 ? 2 : 1) * num_sms();
   return c;
 }
 
@@ -173,14 +176,16 @@ int bsa_paged_forward(const bsa_dims* dims, const void* Q, const int32_t* n_new,
   p.wait_limit_ns = g_wait_limit_ns.load();
   p.withhold_tile = g_withheld_tile.load();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((long long)p.G * p.N > c.rows) return cuda_status(launch_paged_forward(p, s));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const PagedWork w{reinterpret_cast<SplitItem*>(ws + L.split), reinterpret_cast<float2*>(ws + L.ml),
                     reinterpret_cast<float*>(ws + L.o)};
-  CUtensorMap mk, mv;
-  if ((st = make_page_map(&mk, p, p.k, c.keys)) != BSA_OK) return st;
-  if ((st = make_page_map(&mv, p, p.v, c.keys)) != BSA_OK) return st;
-  return cuda_status(launch_paged_rows(mk, mv, p, w, c.grid, s));
+  CUtensorMap mk, mv, mq;
+  const int copy_keys = p.e4m3 ? 64 : c.keys;
+  if ((st = make_page_map(&mk, p, p.k, copy_keys)) != BSA_OK) return st;
+  if ((st = make_page_map(&mv, p, p.v, copy_keys)) != BSA_OK) return st;
+  if (c.rows == 16) return cuda_status(launch_paged_rows(mk, mv, p, w, c.grid, s));
+  if ((st = make_map(&mq, Q, (long long)p.B * p.Hkv, p.G * p.N, p.d)) != BSA_OK) return st;
+  return cuda_status(launch_paged_tiles(mq, mk, mv, p, w, c.rows, c.row_tiles, c.grid, s));
 }
 
 }  // extern "C"

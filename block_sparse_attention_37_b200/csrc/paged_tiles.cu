@@ -1,0 +1,869 @@
+// The paged forward for more than 16 packed query rows a key/value head:
+// chunks of a prompt, blocks of tokens denoised together.
+//
+// Persistent CTAs, one an SM, each walk one run of the line of 128-key tiles
+// (paged_sched.cuh). An item is 256 query rows: two 128-row tiles, one a
+// softmax warpgroup, that share every K and V tile (a causal chunk's upper
+// tile skips the keys only the lower one keeps). With at most 128 rows
+// (SPLIT) both warpgroups hold the same rows and take alternate tiles; their
+// results are joined in the CTA, so the pipe still has two independent
+// softmaxes to work between. Either way the tensor core runs one warpgroup's
+// PV and next QK^T under the other's softmax, and the exponentials (16 a
+// clock and SM, 2048 clocks for a tile of 256 rows) and the products (as many)
+// bound a long chunk; K and V of a short one are bound by HBM.
+// Roles:
+//   warp 0      TMA producer of K (a lane a copy: a page's part of a tile)
+//   warp 1      TMEM allocator and tcgen05.mma issuer
+//   warp 2      TMA producer of V; clears the rows of V no key owns
+//   warp 3      TMA producer of Q, ahead of the item's first product
+//   warps 4-11  the softmax warpgroups
+//   warps 12-15 (e4m3) converters: warp 0 then loads K and V as codes, and
+//               these four turn them into the fp16 tiles the products read
+// Tensor memory: S at 128w with P written over it, O at 256 + Dw.
+//
+// e4m3: K's codes are exact in fp16, its scale multiplies the logits. V is
+// converted as code * scale / sigma (sigma a power of two, the largest V scale
+// of the piece so far), one rounding to fp16's 11 bits; O is rescaled when
+// sigma grows. Q is fp16 after a power-of-two scale of each row. The weights
+// are fp16 times 2^12: what is flushed is below 2^-36 of the largest.
+#include <type_traits>
+
+#include "mma_steps.cuh"
+#include "paged_sched.cuh"
+#include "tiles.cuh"
+
+namespace bsa {
+
+constexpr int kTileKeys = 128;
+constexpr int kTilesMin = 4;  // a run is at least this many tiles
+
+template <int D, bool E4M3>
+struct TilesCfg {
+  static constexpr int THREADS = E4M3 ? 512 : 384;
+  static constexpr int S = D == 64 ? 4 : 2;        // K and V stages
+  static constexpr int TILE = 128 * D * 2;         // 16-bit tile of 128 rows
+  static constexpr int NCH = D / 64;
+  static constexpr int CHUNK = 128 * 128;
+  static constexpr int RAW = E4M3 ? 3 : 0;         // code pieces of 64 keys
+  static constexpr int RAW_BYTES = 64 * D;
+  static constexpr int K_OFF = 2 * TILE;           // after the two Q slots
+  static constexpr int V_OFF = K_OFF + S * TILE;
+  static constexpr int RAW_OFF = V_OFF + S * TILE;
+  static constexpr int LAND_OFF = RAW_OFF + RAW * RAW_BYTES;            // [2][K, V][128] scales as loaded
+  static constexpr int KSC_OFF = LAND_OFF + (E4M3 ? 2 * 2 * 512 : 0);   // [2 S][128] K scales of a tile
+  static constexpr int SIG_OFF = KSC_OFF + (E4M3 ? 2 * S * 512 : 0);    // [2 S] sigma of a tile
+  static constexpr int ML_OFF = SIG_OFF + (E4M3 ? 64 : 0);              // [128] warpgroup 1's (m, l, factor) (SPLIT)
+  static constexpr int ZS_OFF = ML_OFF + 128 * 16;                      // [128] row factors (SPLIT, e4m3)
+  static constexpr int BAR_OFF = ZS_OFF + (E4M3 ? 512 : 0);
+  static constexpr int NBAR = 4 + 1 + 4 * S + 1 + 8 + 1 + 2 * RAW;
+  static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
+  static constexpr int SMEM = MISC_OFF + 16 + sizeof(Run) + 16 * 8;
+  static constexpr int ALLOC = SMEM + 1024;
+  static_assert(ALLOC <= 227 * 1024, "smem budget");
+  // register split: the launch gives every thread REGS; the softmax
+  // warpgroups rise, the others drop
+  static constexpr int REGS = E4M3 ? 128 : 168;
+  static constexpr int REGS_CTL = E4M3 ? 48 : 56;
+  static constexpr int REGS_CNV = 64;
+  static constexpr int REGS_SMX = E4M3 ? 200 : 224;
+  static_assert(128 * REGS_CTL + 256 * REGS_SMX + (E4M3 ? 128 * REGS_CNV : 0) <= THREADS * REGS,
+                "register split exceeds the launch allocation");
+};
+
+// Instruction descriptor for kind::f16 with fp16 A and B and fp32 D.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Which warpgroups need key tile kt (absolute) of a piece, and how many of
+// the piece's tiles each needs. Every role asks the same questions.
+template <bool SPLIT>
+struct TileNeed {
+  int a0, e0, a1, e1;  // tile ranges of the warpgroups
+  int first;           // the piece's first tile (SPLIT)
+  __device__ __forceinline__ TileNeed(const PagedParams& p, const Piece& q) {
+    first = q.s.t0 + q.t;
+    const int end = first + q.m;
+    if constexpr (SPLIT) {
+      const bool any = q.s.lo < q.s.hi;
+      a0 = a1 = first;
+      e0 = e1 = any ? end : first;
+    } else {
+      const ItemSpan x = item_span<128, kTileKeys>(p, q.n, q.kv, 2 * q.rt);
+      ItemSpan y{0, 0, 0, 0, 0, 0};
+      if ((long long)q.rt * 256 + 128 < (long long)p.G * p.N) y = item_span<128, kTileKeys>(p, q.n, q.kv, 2 * q.rt + 1);
+      a0 = max(first, x.t0);
+      e0 = x.lo < x.hi ? min(end, x.t0 + x.nt) : a0;
+      a1 = max(first, y.t0);
+      e1 = y.lo < y.hi ? min(end, y.t0 + y.nt) : a1;
+    }
+  }
+  __device__ __forceinline__ int mask(int kt) const {
+    if constexpr (SPLIT) return kt < e0 ? 1 << ((kt - first) & 1) : 0;
+    return (kt >= a0 && kt < e0 ? 1 : 0) | (kt >= a1 && kt < e1 ? 2 : 0);
+  }
+  __device__ __forceinline__ bool any(int w) const {
+    if constexpr (SPLIT) return e0 - first > w;
+    return w ? e1 > a1 : e0 > a0;
+  }
+};
+
+__device__ __forceinline__ void mul2(float& x0, float& x1, float c0, float c1) {
+  uint64_t v, c;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x0), "f"(x1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(c0), "f"(c1));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(v), "l"(c));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(v));
+}
+
+template <int D, bool E4M3, bool SPLIT>
+__global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
+    paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const PagedParams p, const PagedWork wk,
+                       int row_tiles) {
+  using C = TilesCfg<D, E4M3>;
+  constexpr int S = C::S, ROWS = SPLIT ? 128 : 256;
+  constexpr float kTau = E4M3 ? 3.f : 8.f;    // the state moves when a row's maximum grows by more than 2^kTau
+  constexpr float kGain = E4M3 ? 12.f : 0.f;  // log2 of what the weights are held times
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* sQ = smem;
+  uint8_t* sK = smem + C::K_OFF;
+  uint8_t* sV = smem + C::V_OFF;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);  // [2]
+  uint64_t* q_ready = q_full + 2;    // [2] e4m3: Q converted
+  uint64_t* q_empty = q_ready + 2;   // every QK^T of the piece complete
+  uint64_t* k_full = q_empty + 1;    // [S]
+  uint64_t* k_empty = k_full + S;
+  uint64_t* v_full = k_empty + S;
+  uint64_t* v_empty = v_full + S;
+  uint64_t* v_land = v_empty + S;    // V of a tile with rows to clear
+  uint64_t* s_full = v_land + 1;     // [2]
+  uint64_t* p_full = s_full + 2;     // [2]
+  uint64_t* o_ready = p_full + 2;    // [2]
+  uint64_t* o_free = o_ready + 2;    // [2] O read by the softmax
+  uint64_t* mma_done = o_free + 2;
+  uint64_t* raw_full = mma_done + 1; // [RAW]
+  uint64_t* raw_empty = raw_full + C::RAW;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  Run* run_sh = reinterpret_cast<Run*>(smem + C::MISC_OFF + 16);
+  long long* scan_sh = reinterpret_cast<long long*>(smem + C::MISC_OFF + 16 + sizeof(Run));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (tid == 0) {
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&q_full[w], 1);
+      mbar_init(&q_ready[w], 128);
+      mbar_init(&s_full[w], 1);
+      mbar_init(&p_full[w], 128);
+      mbar_init(&o_ready[w], 1);
+      mbar_init(&o_free[w], 128);
+    }
+    mbar_init(q_empty, 1);
+    mbar_init(v_land, 1);
+    mbar_init(mma_done, 1);
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&k_full[s], E4M3 ? 4 : 1);
+      mbar_init(&v_full[s], E4M3 ? 4 : 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int s = 0; s < C::RAW; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], 4);
+    }
+    misc[1] = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(misc, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  Run run = find_run<ROWS, kTileKeys, C::THREADS>(p, row_tiles, kTilesMin, run_sh, scan_sh);  // block barriers
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+
+  // every role ends with its own copy of the teardown (a shared tail would
+  // make the register allocator apply the control warpgroup's limit to all)
+  auto teardown = [&]() {
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+      tc_fence_after();
+      tmem_dealloc(tmem, 512);
+    }
+  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return warp_all(mbar_wait(bar, parity & 1u, abort_flag, p.wait_limit_ns));
+  };
+  const int page_mask = (1 << p.page_log2) - 1;
+
+  if (warp < 4) {
+    regs_release<C::REGS_CTL>();
+    if (warp == 3) {
+      // ------------------------------------------------------------- Q producer
+      int pc = 0;
+      bool ok = true;
+      for (; run.left > 0 && ok; ++pc) {
+        const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
+        if (pc > 0) {  // the slots are free, and their last tiles have landed
+          ok = wait(q_empty, pc - 1);
+          for (int w = 0; w < (SPLIT ? 1 : 2); ++w) ok = ok && wait(&q_full[w], pc - 1);
+          if (!ok) {
+            cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
+            break;
+          }
+        }
+        if (lane == 0)
+          for (int w = 0; w < (SPLIT ? 1 : 2); ++w) {
+            mbar_arrive_expect_tx(&q_full[w], C::TILE);
+            for (int c = 0; c < C::NCH; ++c)
+              for (int h2 = 0; h2 < 2; ++h2)  // rows past the head's G N read as zeros
+                tma_load_3d(sQ + w * C::TILE + c * C::CHUNK + h2 * (C::CHUNK / 2), &tmQ, &q_full[w], c * 64,
+                            q.rt * ROWS + 128 * w + 64 * h2, q.b * p.Hkv + q.hk);
+          }
+        __syncwarp();
+      }
+      if (*abort_flag && pc > 0 && lane == 0)
+        for (int w = 0; w < (SPLIT ? 1 : 2); ++w) mbar_drain(&q_full[w], (uint32_t)(pc - 1) & 1u);
+    } else if (warp == 0 || (warp == 2 && !E4M3)) {
+      if constexpr (E4M3) {
+        // ------------------------------------------------------- code producer
+        // pieces of 64 keys: K low, K high, V low, V high of every tile; the
+        // tile's scales land with the first
+        const int per = min(page_mask + 1, 64), sub = 64 / per;
+        const int part = lane & 3, role = lane >> 2;  // role 0: codes, 1..4: scales (K, V) x (low, high)
+        int c = 0, k = 0;
+        bool ok = true;
+        while (run.left > 0 && ok) {
+          const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
+          const TileNeed<SPLIT> need(p, q);
+          for (int i = 0; i < q.m && ok; ++i) {
+            const int kt = q.s.t0 + q.t + i;
+            if (need.mask(kt) == 0) continue;
+            for (int x = 0; x < 4; ++x, ++c) {
+              const int half = role == 0 ? x & 1 : (role - 1) & 1;
+              const int j0 = kt * kTileKeys + 64 * half + part * per;
+              const bool mine = part < sub && j0 < q.s.hi && j0 + per > q.s.lo && (role == 0 || (x == 0 && role <= 4));
+              int pg = 0;
+              if (mine) pg = max(page_of(p, q.b, j0), 0);
+              const int st = c % C::RAW;
+              if (c >= C::RAW) ok = wait(&raw_empty[st], c / C::RAW - 1);
+              if (!ok) {
+                cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
+                break;
+              }
+              if (k == p.withhold_tile && x == 0) continue;  // failure-detection test
+              const uint32_t codes = __popc(__ballot_sync(0xffffffffu, mine && role == 0));
+              const uint32_t scales = __popc(__ballot_sync(0xffffffffu, mine && role != 0));
+              if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], codes * per * D + scales * per * 4);
+              __syncwarp();
+              if (mine) {
+                if (role == 0)
+                  tma_load_3d(smem + C::RAW_OFF + st * C::RAW_BYTES + part * per * D, x < 2 ? &tmK : &tmV, &raw_full[st],
+                              0, (j0 & page_mask) * D / 128, pg * p.Hkv + q.hk);
+                else
+                  bulk_load_1d(smem + C::LAND_OFF + ((k & 1) * 2 + ((role - 1) >> 1)) * 512 + (64 * half + part * per) * 4,
+                               (role <= 2 ? p.k_scale : p.v_scale) + cache_row(p, pg, q.hk, j0), per * 4, &raw_full[st]);
+              }
+              __syncwarp();
+            }
+            ++k;
+          }
+        }
+        if (*abort_flag && lane == 0)
+          for (int t = max(0, c - C::RAW); t < c; ++t)
+            if (t != 4 * p.withhold_tile) mbar_drain(&raw_full[t % C::RAW], (uint32_t)(t / C::RAW) & 1u);
+      } else {
+        // ------------------------------------------------------- K and V producers
+        auto produce = [&](auto ring) {
+          constexpr bool IS_K = decltype(ring)::value;
+          uint64_t* const full = IS_K ? k_full : v_full;
+          uint64_t* const empty = IS_K ? k_empty : v_empty;
+          const int per = min(page_mask + 1, kTileKeys), sub = kTileKeys / per;
+          const int part = lane / C::NCH, ch = lane % C::NCH;
+          int k = 0, landed = 0;
+          bool ok = true;
+          while (run.left > 0 && ok) {
+            const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
+            const TileNeed<SPLIT> need(p, q);
+            for (int i = 0; i < q.m; ++i) {
+              const int kt = q.s.t0 + q.t + i;
+              if (need.mask(kt) == 0) continue;
+              const int st = k % S, key0 = kt * kTileKeys;
+              const int j0 = key0 + part * per;
+              const bool mine = part < sub && j0 < q.s.hi && j0 + per > q.s.lo;
+              int pg = 0;
+              if (mine) pg = max(page_of(p, q.b, j0), 0);
+              if (k >= S) ok = wait(&empty[st], k / S - 1);
+              if (!ok) {
+                cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
+                break;
+              }
+              if (IS_K && k == p.withhold_tile) {  // failure-detection test
+                ++k;
+                continue;
+              }
+              // V rows of no kept key: their weights are zero, but whatever
+              // the slots hold (NaN, even) must not meet them
+              const bool clear = !IS_K && (key0 < q.s.lo || key0 + kTileKeys > q.s.hi);
+              uint64_t* bar = clear ? v_land : &full[st];
+              const uint32_t copies = __popc(__ballot_sync(0xffffffffu, mine));
+              if (lane == 0) mbar_arrive_expect_tx(bar, copies * per * 128);
+              __syncwarp();
+              uint8_t* tile = (IS_K ? sK : sV) + st * C::TILE;
+              if (mine)
+                tma_load_3d(tile + ch * C::CHUNK + part * per * 128, IS_K ? &tmK : &tmV, bar, ch * 64, j0 & page_mask,
+                            pg * p.Hkv + q.hk);
+              __syncwarp();
+              if (clear) {
+                ok = wait(v_land, landed++);
+                if (!ok) {
+                  cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
+                  if (lane == 0) mbar_drain(v_land, (uint32_t)(landed - 1) & 1u);
+                  break;
+                }
+                const int a = max(q.s.lo - key0, 0), e = min(q.s.hi - key0, kTileKeys);  // rows [a, e) stay
+                for (int x = lane; x < (kTileKeys - (e - a)) * 8 * C::NCH; x += 32) {
+                  const int u = x % (8 * C::NCH), r0 = x / (8 * C::NCH);
+                  const int r = r0 < a ? r0 : r0 - a + e;
+                  *reinterpret_cast<uint4*>(tile + (u >> 3) * C::CHUNK + r * 128 + (u & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[st]);
+              }
+              ++k;
+            }
+          }
+          // copies in flight land before the CTA ends; a stage whose tile was
+          // cleared by this warp has landed already
+          if (*abort_flag && lane == 0)
+            for (int t = max(0, k - S); t < k; ++t)
+              if (!IS_K || t != p.withhold_tile) mbar_drain(&full[t % S], (uint32_t)(t / S) & 1u);
+        };
+        if (warp == 0)
+          produce(std::true_type{});
+        else
+          produce(std::false_type{});
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------- MMA issuer
+      constexpr uint32_t idesc_qk = E4M3 ? idesc_f16_f32(128, 128, false) : idesc_bf16_f32(128, 128, false, false);
+      constexpr uint32_t idesc_pv = E4M3 ? idesc_f16_f32(128, D, true) : idesc_bf16_f32(128, D, false, true);
+      const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV);
+      int pt0 = -1, pt1 = -1;    // tile whose PV is outstanding, per warpgroup
+      int np0 = 0, np1 = 0;      // PVs issued
+      int nf0 = 0, nf1 = 0;      // pieces begun
+      bool new0 = false, new1 = false;  // the next PV is the piece's first
+      int v_seen = 0, k = 0, pc = 0;
+      uint32_t rem = 0u;         // warpgroups still to use a stage's V, two bits a stage
+      bool ok = true, issued = false;
+      // V tiles are observed in tile order, so the parity test never meets
+      // another phase of a shared stage
+      auto pv = [&](int w) -> bool {
+        const int u = w ? pt1 : pt0, st = u % S;
+        for (; v_seen <= u; ++v_seen)
+          if (!wait(&v_full[v_seen % S], v_seen / S)) return false;
+        bool& fresh = w ? new1 : new0;
+        if (fresh) {  // O of the piece before has been read
+          int& nf = w ? nf1 : nf0;
+          if (nf > 0 && !wait(&o_free[w], nf - 1)) return false;
+          ++nf;
+        }
+        int& np = w ? np1 : np0;
+        if (!wait(&p_full[w], np)) return false;
+        ++np;
+        tc_fence_after();
+        pv_all(tmem + 256 + w * D, tmem + 128 * w, smem_desc_sw128(sVa + st * C::TILE, C::CHUNK, 1024), idesc_pv,
+               fresh ? 1u : 0u, std::make_integer_sequence<int, 8>{});
+        fresh = false;
+        tc_commit_warp(&o_ready[w]);
+        rem -= 1u << (2 * st);
+        if (((rem >> (2 * st)) & 3u) == 0u) tc_commit_warp(&v_empty[st]);
+        (w ? pt1 : pt0) = -1;
+        return true;
+      };
+      // outstanding PVs of tiles below `limit`, oldest first
+      auto flush_below = [&](int limit) -> bool {
+        const bool f0 = pt0 >= 0 && pt0 < limit, f1 = pt1 >= 0 && pt1 < limit;
+        if (f0 && f1 && pt1 < pt0) return pv(1) && pv(0);
+        return (!f0 || pv(0)) && (!f1 || pv(1));
+      };
+      auto qk = [&](int w, int st) {
+        tc_fence_after();
+        qk_all(tmem + 128 * w, smem_desc_sw128(sQa + (SPLIT ? 0 : w) * C::TILE, 16, 1024),
+               smem_desc_sw128(sKa + st * C::TILE, 16, 1024), idesc_qk, std::make_integer_sequence<int, D / 16>{});
+        tc_commit_warp(&s_full[w]);
+        issued = true;
+      };
+      for (; run.left > 0 && ok; ++pc) {
+        const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
+        const TileNeed<SPLIT> need(p, q);
+        for (int w = 0; w < (SPLIT ? 1 : 2) && ok; ++w) ok = wait(E4M3 ? &q_ready[w] : &q_full[w], pc);
+        new0 = new1 = true;
+        for (int i = 0; i < q.m && ok; ++i) {
+          const int nw = need.mask(q.s.t0 + q.t + i);
+          if (nw == 0) continue;
+          const int st = k % S;
+          ok = wait(&k_full[st], k / S) && flush_below(k - S + 1);
+          if (!ok) break;
+          rem |= (uint32_t)__popc(nw) << (2 * st);
+          if (nw & 1) {
+            if (pt0 >= 0 && !(ok = pv(0))) break;
+            qk(0, st);
+            pt0 = k;
+          }
+          if (nw & 2) {
+            if (pt1 >= 0 && !(ok = pv(1))) break;
+            qk(1, st);
+            pt1 = k;
+          }
+          tc_commit_warp(&k_empty[st]);
+          ++k;
+        }
+        if (!ok) break;
+        tc_commit_warp(q_empty);
+        ok = flush_below(k);
+      }
+      if (!ok) cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
+      // tensor memory is freed only once every issued MMA has completed
+      if (issued) {
+        tc_commit_warp(mma_done);
+        mbar_drain(mma_done, 0u);
+      }
+    }
+    teardown();
+  } else if (warp < 12) {
+    regs_claim<C::REGS_SMX>();
+    // --------------------------------------------------------------- softmax
+    const int w = (warp - 4) >> 2, q4 = warp & 3;
+    const int r = q4 * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    const uint32_t stm = tmem + lane_off + 128 * w, otm = tmem + lane_off + 256 + w * D;
+    const int slot_row = (SPLIT ? 0 : 128 * w) + r;  // row of the item
+    float4* ml_sh = reinterpret_cast<float4*>(smem + C::ML_OFF);
+    float* zs_sh = reinterpret_cast<float*>(smem + C::ZS_OFF);
+    int j = 0, k = 0, pc = 0;  // tiles of this warpgroup, tiles and pieces of the CTA
+    bool ok = true;
+    SplitItem split{0, 0, 0, 0};
+    for (; run.left > 0; ++pc) {
+      const long long at = run.pos;
+      const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
+      if (q.t == 0 && q.m < q.s.nt)
+        split = SplitItem{q.b * row_tiles + q.rt, q.hk, run_of(run.total, at + q.s.nt - 1, run.ctas) - (int)blockIdx.x + 1, 0};
+      const TileNeed<SPLIT> need(p, q);
+      const int R = q.rt * ROWS + slot_row;  // packed row of the head
+      const int tok = R < p.G * p.N ? R - fdiv(R, p.f_n) * p.N : 0;
+      const bool written = R < p.G * p.N && tok < q.n;
+      const bool warp_rows = __any_sync(0xffffffffu, written);
+      int lo, hi;
+      row_keys(p, q.n, q.kv, tok, lo, hi);
+      if (!written) lo = hi = 0;
+      // keys that every written row of the warp keeps
+      const int clo = __reduce_max_sync(0xffffffffu, written ? lo : 0);
+      const int chi = __reduce_min_sync(0xffffffffu, written ? hi : 0x7fffffff);
+      float zs = p.scale_log2;
+      if constexpr (E4M3) {
+        if (!SPLIT || w == 0) {
+          // Q to fp16 in place, this thread's row after a power-of-two scale
+          // (exact down to 2^-24 of the row's largest value)
+          ok = ok && wait(&q_full[w], pc);
+          if (ok) {
+            uint8_t* row = sQ + (SPLIT ? 0 : w) * C::TILE + r * 128;
+            uint32_t top = 0u;
+#pragma unroll
+            for (int u = 0; u < D / 8; ++u) {
+              const uint4 x = *reinterpret_cast<const uint4*>(row + (u >> 3) * C::CHUNK + (((u ^ r) & 7) << 4));
+              const uint32_t y = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                          __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+              top = max(top, max(y & 0xffffu, y >> 16));
+            }
+            const int ex = min(max((int)(top >> 7), 1), 253);
+            const float down = __int_as_float((254 - ex) << 23);
+            zs *= __int_as_float(ex << 23);
+#pragma unroll
+            for (int u = 0; u < D / 8; ++u) {
+              uint4* at4 = reinterpret_cast<uint4*>(row + (u >> 3) * C::CHUNK + (((u ^ r) & 7) << 4));
+              uint4 x = *at4;
+              auto half2 = [&](uint32_t v) {
+                return pack_f16x2(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xffff0000u) * down);
+              };
+              *at4 = make_uint4(half2(x.x), half2(x.y), half2(x.z), half2(x.w));
+            }
+            if constexpr (SPLIT) zs_sh[r] = zs;
+          } else {
+            cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&q_ready[w]);
+        } else {
+          // the other warpgroup converts; it cannot pass this piece's join
+          // before this one
+          ok = ok && wait(&q_ready[0], pc);
+          zs = zs_sh[r];
+        }
+      }
+      float m = kNegInf, l = 0.f, sig = 1.f;
+      int jp = 0;  // tiles of this warpgroup in the piece
+      for (int i = 0; i < q.m && ok; ++i) {
+        const int kt = q.s.t0 + q.t + i;
+        const int nw = need.mask(kt);
+        if (nw == 0) continue;
+        const int kk = k++;
+        if (!((nw >> w) & 1)) continue;
+        ok = wait(&s_full[w], j);
+        if (!ok) break;
+        tc_fence_after();
+        if (warp_rows) {
+          const int key0 = kt * kTileKeys;
+          float sv[128];
+          tmem_ld32(stm, sv);
+          tmem_ld32(stm + 32, sv + 32);
+          tmem_ld32(stm + 64, sv + 64);
+          tmem_ld32(stm + 96, sv + 96);
+          tc_wait_ld();
+          float beta = 1.f;
+          if constexpr (E4M3) {
+            const float4* ks = reinterpret_cast<const float4*>(smem + C::KSC_OFF + (kk % (2 * S)) * 512);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const float4 s4 = ks[c];
+              mul2(sv[4 * c], sv[4 * c + 1], s4.x, s4.y);
+              mul2(sv[4 * c + 2], sv[4 * c + 3], s4.z, s4.w);
+            }
+            const float now = *reinterpret_cast<const float*>(smem + C::SIG_OFF + (kk % (2 * S)) * 4);
+            if (jp > 0) beta = sig / now;  // both powers of two
+            sig = now;
+          }
+          if (key0 < clo || key0 + kTileKeys > chi) {
+            const int a = lo - key0, n = hi - lo;
+#pragma unroll
+            for (int c = 0; c < 128; ++c) sv[c] = (uint32_t)(c - a) < (uint32_t)n ? sv[c] : kNegInf;
+          }
+          float x0 = max3f(sv[0], sv[1], sv[2]), x1 = max3f(sv[3], sv[4], sv[5]);
+          float x2 = max3f(sv[64], sv[65], sv[66]), x3 = max3f(sv[67], sv[68], sv[69]);
+#pragma unroll
+          for (int c = 6; c < 62; c += 4) {
+            x0 = max3f(x0, sv[c], sv[c + 1]);
+            x1 = max3f(x1, sv[c + 2], sv[c + 3]);
+            x2 = max3f(x2, sv[64 + c], sv[65 + c]);
+            x3 = max3f(x3, sv[66 + c], sv[67 + c]);
+          }
+          const float top = max3f(max3f(x0, x1, x2), x3, max3f(sv[62], sv[63], fmaxf(sv[126], sv[127]))) * zs;
+          float alpha = 1.f;
+          if (top > m + kTau) {
+            alpha = fast_exp2(m - top);
+            m = top;
+          }
+          const float off = kGain - (m == kNegInf ? 0.f : m);
+          // P over S, chunk by chunk: S(j) landing implies PV(j-1) is complete
+          float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float a = sv[32 * c + 2 * e], b = sv[32 * c + 2 * e + 1];
+              fma2(a, b, zs, off);
+              a = fast_exp2(a);
+              b = fast_exp2(b);
+              add2(sum0, sum1, a, b);
+              pk[e] = E4M3 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+            }
+            tmem_st16(stm + 16 * c, pk);
+          }
+          l = l * alpha + (sum0 + sum1);
+          alpha *= beta;
+          if (jp > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              float o[16];
+              tmem_ld16(otm + c * 16, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= alpha;
+              tmem_st16(otm + c * 16, reinterpret_cast<uint32_t*>(o));
+            }
+          }
+          tc_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(&p_full[w]);
+        ++j;
+        ++jp;
+      }
+      if (ok && jp > 0) {
+        ok = wait(&o_ready[w], j - 1);
+        tc_fence_after();
+      }
+      if (!ok) cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
+      const bool have = ok && jp > 0;
+
+      // ------------------------------------------------------------ epilogue
+      const bool whole = q.whole();
+      const size_t slot = 2 * (size_t)blockIdx.x + (q.t == 0 ? 1 : 0);
+      const size_t obase = ((size_t)(q.b * p.Hkv + q.hk) * p.G * p.N + R) * D;
+      // 32 channels of a row, scaled and stored: the output, or a partial result
+      auto store = [&](int c, float (&o)[32], float f) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] *= f;
+        if (!written) return;
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(p.O + obase + c * 32);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dst[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                                pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+        } else {
+          // [slot][four channels][row]: a warp's rows side by side
+          float4* dst = reinterpret_cast<float4*>(wk.o) + (slot * (D / 4) + c * 8) * ROWS + slot_row;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dst[e * ROWS] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      };
+      auto load = [&](int c, float (&o)[32]) {
+        if (have) {
+          tmem_ld32(otm + c * 32, o);
+          tc_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        }
+      };
+      const float unit = E4M3 ? sig * (1.f / 128.f) : 1.f;  // what O is held over
+      auto inverse = [&](float x) { return !whole ? 1.f : x > 0.f ? 1.f / x : x == 0.f ? 0.f : x; };
+      if constexpr (SPLIT) {
+        // warpgroup 1 hands its half over through the unused Q slot, half of
+        // the channels at a time
+        float4* xch = reinterpret_cast<float4*>(sQ + C::TILE);
+        float f0 = 0.f, f1 = 0.f;
+        if (w == 1) ml_sh[r] = make_float4(m, l, unit, 0.f);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if (w == 1) {
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
+              float o[32];
+              load(h * (D / 64) + c, o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                xch[(c * 8 + e) * 128 + r] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+          }
+          named_bar(3, 256);
+          if (w == 0) {
+            if (h == 0) {
+              const float4 x = ml_sh[r];
+              const float M = fmaxf(m, x.x), mu = M == kNegInf ? 0.f : M;
+              const float e0 = fast_exp2(m - mu), e1 = fast_exp2(x.x - mu);
+              m = M;
+              l = l * e0 + x.y * e1;
+              f0 = e0 * unit * inverse(l);
+              f1 = e1 * x.z * inverse(l);
+            }
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
+              float o[32];
+              load(h * (D / 64) + c, o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 x = xch[(c * 8 + e) * 128 + r];
+                o[4 * e] = o[4 * e] * f0 + x.x * f1;
+                o[4 * e + 1] = o[4 * e + 1] * f0 + x.y * f1;
+                o[4 * e + 2] = o[4 * e + 2] * f0 + x.z * f1;
+                o[4 * e + 3] = o[4 * e + 3] * f0 + x.w * f1;
+              }
+              store(h * (D / 64) + c, o, 1.f);
+            }
+          }
+          named_bar(3, 256);
+        }
+      } else {
+        const float f = unit * inverse(l);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          load(c, o);
+          store(c, o, f);
+        }
+      }
+      if (!whole && written && (!SPLIT || w == 0)) wk.ml[slot * ROWS + slot_row] = make_float2(m, l);
+      if (need.any(w)) {
+        tc_fence_before();
+        mbar_arrive(&o_free[w]);
+      }
+    }
+    if (warp == 4 && lane == 0) wk.split[blockIdx.x] = split;
+    teardown();
+  } else {
+    if constexpr (E4M3) {
+      regs_release<C::REGS_CNV>();
+      // ------------------------------------------------------------- converters
+      const int cw = warp - 12;
+      int c = 0, k = 0;
+      bool ok = true;
+      while (run.left > 0 && ok) {
+        const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
+        const TileNeed<SPLIT> need(p, q);
+        float sig = 0x1p-112f;
+        for (int i = 0; i < q.m && ok; ++i) {
+          const int kt = q.s.t0 + q.t + i;
+          if (need.mask(kt) == 0) continue;
+          const int st = k % S, key0 = kt * kTileKeys;
+          const bool edge = key0 < q.s.lo || key0 + kTileKeys > q.s.hi;
+          const float* land = reinterpret_cast<const float*>(smem + C::LAND_OFF + (k & 1) * 1024);
+          for (int x = 0; x < 4; ++x, ++c) {
+            const int half = x & 1;
+            const bool is_v = x >= 2;
+            ok = wait(&raw_full[c % C::RAW], c / C::RAW);
+            if (ok && half == 0 && k >= S) ok = wait(is_v ? &v_empty[st] : &k_empty[st], k / S - 1);
+            if (!ok) {
+              cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
+              break;
+            }
+            if (x == 0) {
+              // sigma from the tile's V scales (every warp finds the same),
+              // and K's scales into the ring that lives until the tile's PVs
+              const int j4 = key0 + 4 * lane;
+              const float4 f = reinterpret_cast<const float4*>(land + 128)[lane];
+              const float fs[4] = {f.x, f.y, f.z, f.w};
+              uint32_t top = 0u;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t b = __float_as_uint(fs[e]);
+                if (b < 0x7f800000u && (!edge || (j4 + e >= q.s.lo && j4 + e < q.s.hi))) top = max(top, b);
+              }
+              top = __reduce_max_sync(0xffffffffu, top);
+              if (top > __float_as_uint(sig)) sig = __uint_as_float(min((top + 0x7fffffu) & 0x7f800000u, 0x7f000000u));
+              reinterpret_cast<float*>(smem + C::KSC_OFF + (k % (2 * S)) * 512)[32 * cw + lane] = land[32 * cw + lane];
+              if (cw == 0 && lane == 0) *reinterpret_cast<float*>(smem + C::SIG_OFF + (k % (2 * S)) * 4) = sig;
+            }
+            const uint8_t* raw = smem + C::RAW_OFF + (c % C::RAW) * C::RAW_BYTES;
+            uint8_t* tile = (is_v ? sV : sK) + st * C::TILE;
+            constexpr int UNITS = D / 16;                  // 16-code units of a token
+            constexpr int STEP = 128 / UNITS;              // tokens a step of the warpgroup covers
+            const int u = lane % UNITS;
+            const float up = 128.f / sig;
+#pragma unroll
+            for (int e = 0; e < 64 / STEP; ++e) {
+              const int key = e * STEP + cw * (32 / UNITS) + lane / UNITS;  // of the piece
+              const uint32_t lin = key * D + u * 16;
+              uint4 y = *reinterpret_cast<const uint4*>(raw + (lin ^ ((lin >> 3) & 0x70u)));
+              uint32_t h[8] = {codes_lo(y.x), codes_hi(y.x), codes_lo(y.y), codes_hi(y.y),
+                               codes_lo(y.z), codes_hi(y.z), codes_lo(y.w), codes_hi(y.w)};
+              const int row = 64 * half + key;
+              if (is_v) {
+                const float s = land[128 + row] * up;
+                const uint32_t s2 = pack_f16x2(s, s);
+                const bool out = edge && (key0 + row < q.s.lo || key0 + row >= q.s.hi);
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                  const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&h[n]), *reinterpret_cast<const __half2*>(&s2));
+                  h[n] = out ? 0u : *reinterpret_cast<const uint32_t*>(&z);
+                }
+              }
+              uint8_t* dst = tile + (u >> 2) * C::CHUNK + row * 128;
+              const int a = 2 * (u & 3);
+              *reinterpret_cast<uint4*>(dst + (((a ^ row) & 7) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(dst + ((((a + 1) ^ row) & 7) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&raw_empty[c % C::RAW]);
+              if (half == 1) mbar_arrive(is_v ? &v_full[st] : &k_full[st]);
+            }
+          }
+          ++k;
+        }
+      }
+      teardown();
+    }
+  }
+}
+
+// Joins the partial results of split items (see paged_join_kernel): grid
+// (CTAs of the forward, y), a thread a row and four channels, rows side by
+// side as they were stored.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256) paged_join_tiles_kernel(const PagedParams p, const PagedWork wk, int row_tiles) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const SplitItem it = wk.split[blockIdx.x];
+  if (it.parts <= 1) return;
+  const int b = it.idx / row_tiles, rt = it.idx - b * row_tiles;
+  const SeqLen s = clamp_lens(p, p.n_new ? __ldg(p.n_new + b) : p.N, __ldg(p.kv_len + b));
+  auto slot = [&](int i) -> size_t { return i == 0 ? 2 * (size_t)blockIdx.x + 1 : 2 * ((size_t)blockIdx.x + i); };
+  for (int x = blockIdx.y * 256 + threadIdx.x; x < ROWS * (D / 4); x += gridDim.y * 256) {
+    const int r = x % ROWS, c4 = x / ROWS;
+    const int R = rt * ROWS + r;
+    if (R >= p.G * p.N || R - fdiv(R, p.f_n) * p.N >= s.n) continue;
+    float m = kNegInf, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < it.parts; ++i) {
+      const float2 ml = wk.ml[slot(i) * ROWS + r];
+      const float4 o = reinterpret_cast<const float4*>(wk.o)[(slot(i) * (D / 4) + c4) * ROWS + r];
+      const float M = fmaxf(m, ml.x), mu = M == kNegInf ? 0.f : M;
+      const float e0 = fast_exp2(m - mu), e1 = fast_exp2(ml.x - mu);
+      m = M;
+      l = l * e0 + ml.y * e1;
+      acc.x = acc.x * e0 + o.x * e1;
+      acc.y = acc.y * e0 + o.y * e1;
+      acc.z = acc.z * e0 + o.z * e1;
+      acc.w = acc.w * e0 + o.w * e1;
+    }
+    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+    const size_t at = ((size_t)(b * p.Hkv + it.hk) * p.G * p.N + R) * D + 4 * c4;
+    *reinterpret_cast<uint2*>(p.O + at) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  }
+}
+
+template <int D, bool E4M3, bool SPLIT>
+static cudaError_t launch_tiles_d(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                                  const PagedParams& p, const PagedWork& w, int row_tiles, int grid,
+                                  cudaStream_t stream) {
+  using C = TilesCfg<D, E4M3>;
+  auto fn = paged_tiles_kernel<D, E4M3, SPLIT>;
+  static DeviceOnce once;
+  cudaError_t e = once.run([&]() -> cudaError_t {
+    // the register split needs the full launch allocation: a smaller one
+    // would leave setmaxnreg.inc waiting, so refuse to launch instead
+    cudaFuncAttributes fa;
+    cudaError_t r = cudaFuncGetAttributes(&fa, fn);
+    if (r != cudaSuccess) return r;
+    if (fa.numRegs != C::REGS) return cudaErrorInvalidKernelImage;
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
+  });
+  if (e != cudaSuccess) return e;
+  fn<<<grid, C::THREADS, C::ALLOC, stream>>>(q, k, v, p, w, row_tiles);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  constexpr int ROWS = SPLIT ? 128 : 256;
+  return launch_after(paged_join_tiles_kernel<D, ROWS>, dim3(grid, 8), 256, stream, p, w, row_tiles);
+}
+
+template <int D, bool E4M3>
+static cudaError_t launch_tiles_any(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                                    const PagedParams& p, const PagedWork& w, int rows, int row_tiles, int grid,
+                                    cudaStream_t stream) {
+  return rows == 128 ? launch_tiles_d<D, E4M3, true>(q, k, v, p, w, row_tiles, grid, stream)
+                     : launch_tiles_d<D, E4M3, false>(q, k, v, p, w, row_tiles, grid, stream);
+}
+
+cudaError_t launch_paged_tiles(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p,
+                               const PagedWork& w, int rows, int row_tiles, int grid, cudaStream_t stream) {
+  if (p.d == 64)
+    return p.e4m3 ? launch_tiles_any<64, true>(q, k, v, p, w, rows, row_tiles, grid, stream)
+                  : launch_tiles_any<64, false>(q, k, v, p, w, rows, row_tiles, grid, stream);
+  return p.e4m3 ? launch_tiles_any<128, true>(q, k, v, p, w, rows, row_tiles, grid, stream)
+                : launch_tiles_any<128, false>(q, k, v, p, w, rows, row_tiles, grid, stream);
+}
+
+}  // namespace bsa
