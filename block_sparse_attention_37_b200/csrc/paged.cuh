@@ -67,6 +67,18 @@ __device__ __forceinline__ int page_of(const PagedParams& p, int b, int j) {
   return pg;
 }
 
+// The same in two steps, for producers that look a tile ahead: the entry is
+// read early and checked when the copy goes out; an index outside the cache
+// is recorded and page 0 read in its place.
+__device__ __forceinline__ int table_entry(const PagedParams& p, int b, int j) {
+  return __ldg(p.table + (size_t)b * p.max_pages + (j >> p.page_log2));
+}
+__device__ __forceinline__ int checked_page(const PagedParams& p, int entry) {
+  if (entry >= 0 && entry < p.n_pages) return entry;
+  record_error(BSA_DEVERR_BAD_INDEX);
+  return 0;
+}
+
 // Row (token and head) index of slot j % page of page pg: rows hold d values.
 __host__ __device__ __forceinline__ long long cache_row(const PagedParams& p, int pg, int hk, int j) {
   return (((long long)pg * p.Hkv + hk) << p.page_log2) + (j & ((1 << p.page_log2) - 1));

@@ -162,13 +162,14 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
     bool ok = true;
     while (run.left > 0 && ok) {
       const Piece q = next_piece<kRowsTile, kRowsKeys>(p, 1, run);
-      for (int i = 0; i < q.m; ++i, ++k) {
+      int j0 = (q.s.t0 + q.t) * kRowsKeys + piece * per;  // first token of this lane's copies
+      auto keeps = [&](int j) { return piece < sub && j < q.s.hi && j + per > q.s.lo; };
+      int next = keeps(j0) ? table_entry(p, q.b, j0) : 0;
+      for (int i = 0; i < q.m; ++i, ++k, j0 += kRowsKeys) {
         const int st = k % S;
-        const int key0 = (q.s.t0 + q.t + i) * kRowsKeys;
-        const int j0 = key0 + piece * per;
-        const bool mine = piece < sub && j0 < q.s.hi && j0 + per > q.s.lo;
-        int pg = 0;
-        if (mine) pg = max(page_of(p, q.b, j0), 0);
+        const bool mine = keeps(j0);
+        const int entry = next;  // the next tile's is on its way while this one waits for its stage
+        next = i + 1 < q.m && keeps(j0 + kRowsKeys) ? table_entry(p, q.b, j0 + kRowsKeys) : 0;
         if (k >= S) ok = warp_all(mbar_wait(&empty[st], (uint32_t)(k / S - 1) & 1u, abort_flag, p.wait_limit_ns));
         if (!ok) {
           cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
         if (lane == 0) mbar_arrive_expect_tx(&full[st], copies * copy_bytes);
         __syncwarp();
         if (mine) {
+          const int pg = checked_page(p, entry);
           uint8_t* dk = smem + st * C::STAGE;
           const int slot = j0 & ((1 << p.page_log2) - 1);
           const int z = pg * p.Hkv + q.hk;

@@ -244,15 +244,25 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
         while (run.left > 0 && ok) {
           const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
           const TileNeed<SPLIT> need(p, q);
+          // lane l < 2 sub holds the table entry of tokens l per .. of a tile;
+          // the next tile's is on its way while this one's pieces wait
+          auto keeps = [&](int j) { return j < q.s.hi && j + per > q.s.lo; };
+          auto entry_of = [&](int kt) {
+            const int j = kt * kTileKeys + lane * per;
+            return lane < 2 * sub && keeps(j) ? table_entry(p, q.b, j) : 0;
+          };
+          int next = entry_of(q.s.t0 + q.t);
           for (int i = 0; i < q.m && ok; ++i) {
             const int kt = q.s.t0 + q.t + i;
+            const int entry = next;
+            if (i + 1 < q.m) next = entry_of(kt + 1);
             if (need.mask(kt) == 0) continue;
+            const int page = lane < 2 * sub && keeps(kt * kTileKeys + lane * per) ? checked_page(p, entry) : 0;
             for (int x = 0; x < 4; ++x, ++c) {
               const int half = role == 0 ? x & 1 : (role - 1) & 1;
               const int j0 = kt * kTileKeys + 64 * half + part * per;
-              const bool mine = part < sub && j0 < q.s.hi && j0 + per > q.s.lo && (role == 0 || (x == 0 && role <= 4));
-              int pg = 0;
-              if (mine) pg = max(page_of(p, q.b, j0), 0);
+              const bool mine = part < sub && keeps(j0) && (role == 0 || (x == 0 && role <= 4));
+              const int pg = __shfl_sync(0xffffffffu, page, half * sub + part);
               const int st = c % C::RAW;
               if (c >= C::RAW) ok = wait(&raw_empty[st], c / C::RAW - 1);
               if (!ok) {
@@ -293,14 +303,16 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
           while (run.left > 0 && ok) {
             const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
             const TileNeed<SPLIT> need(p, q);
-            for (int i = 0; i < q.m; ++i) {
+            int j0 = (q.s.t0 + q.t) * kTileKeys + part * per;  // first token of this lane's copies
+            auto keeps = [&](int j) { return part < sub && j < q.s.hi && j + per > q.s.lo; };
+            int next = keeps(j0) ? table_entry(p, q.b, j0) : 0;
+            for (int i = 0; i < q.m; ++i, j0 += kTileKeys) {
               const int kt = q.s.t0 + q.t + i;
+              const bool mine = keeps(j0);
+              const int entry = next;  // the next tile's is on its way while this one waits for its stage
+              next = i + 1 < q.m && keeps(j0 + kTileKeys) ? table_entry(p, q.b, j0 + kTileKeys) : 0;
               if (need.mask(kt) == 0) continue;
               const int st = k % S, key0 = kt * kTileKeys;
-              const int j0 = key0 + part * per;
-              const bool mine = part < sub && j0 < q.s.hi && j0 + per > q.s.lo;
-              int pg = 0;
-              if (mine) pg = max(page_of(p, q.b, j0), 0);
               if (k >= S) ok = wait(&empty[st], k / S - 1);
               if (!ok) {
                 cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
@@ -320,7 +332,7 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
               uint8_t* tile = (IS_K ? sK : sV) + st * C::TILE;
               if (mine)
                 tma_load_3d(tile + ch * C::CHUNK + part * per * 128, IS_K ? &tmK : &tmV, bar, ch * 64, j0 & page_mask,
-                            pg * p.Hkv + q.hk);
+                            checked_page(p, entry) * p.Hkv + q.hk);
               __syncwarp();
               if (clear) {
                 ok = wait(v_land, landed++);
