@@ -56,25 +56,26 @@ int paged_forward_params(const bsa_dims* dims, const bsa_paged_cache* c, PagedPa
   return BSA_OK;
 }
 
-// The cache's K or V for TMA: 128-byte rows of pages in boxes of a page's part
-// of a `keys`-token tile (a token's row is one or two 64-channel halves, or
-// half a 128-byte row for e4m3 codes at d = 64), 128-byte swizzle.
-int make_page_map(CUtensorMap* m, const PagedParams& p, const void* base, int keys) {
+// The cache's K or V for TMA, in boxes of a page's part of a `keys`-token
+// tile: rows of 128 bytes, 128-byte swizzle (a bf16 token is one or two
+// 64-channel halves; e4m3 codes at d = 64 lie two tokens a row). `rows64`:
+// e4m3 at d = 64 as rows of 64 bytes, 64-byte swizzle (an MMA operand).
+int make_page_map(CUtensorMap* m, const PagedParams& p, const void* base, int keys, bool rows64 = false) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return BSA_ERR_CUDA;
   const int page = 1 << p.page_log2;
   const int box_tokens = page < keys ? page : keys;
-  const bool half = p.e4m3 && p.d == 64;  // two tokens a 128-byte row
-  const cuuint64_t inner = p.e4m3 ? 128 : p.d, rows = half ? page / 2 : page;
-  const cuuint64_t row_bytes = p.e4m3 ? 128 : (cuuint64_t)p.d * 2;
+  const bool half = p.e4m3 && p.d == 64 && !rows64;  // two tokens a 128-byte row
+  const cuuint64_t inner = !p.e4m3 ? p.d : rows64 ? 64 : 128, rows = half ? page / 2 : page;
+  const cuuint64_t row_bytes = p.e4m3 ? inner : inner * 2;
   cuuint64_t dims[3] = {inner, rows, (cuuint64_t)p.n_pages * p.Hkv};
   cuuint64_t strides[2] = {row_bytes, rows * row_bytes};
-  cuuint32_t box[3] = {p.e4m3 ? 128u : 64u, (cuuint32_t)(half ? box_tokens / 2 : box_tokens), 1};
+  cuuint32_t box[3] = {p.e4m3 ? (cuuint32_t)inner : 64u, (cuuint32_t)(half ? box_tokens / 2 : box_tokens), 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(m, p.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  rows64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? BSA_OK : BSA_ERR_CUDA;
 }
 
@@ -89,7 +90,7 @@ PagedCut paged_cut(const PagedParams& p) {
   const long long rows = (long long)p.G * p.N;
   PagedCut c;
   c.rows = rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
-  c.keys = c.rows == 16 ? 64 : 128;  // tile of the line (e4m3 codes are copied 64 keys at a time)
+  c.keys = c.rows == 16 ? 64 : 128;
   c.row_tiles = ceil_div(rows, c.rows);
   c.grid = (c.rows == 16 ? 2 : 1) * num_sms();
   return c;
@@ -180,10 +181,11 @@ int bsa_paged_forward(const bsa_dims* dims, const void* Q, const int32_t* n_new,
   const PagedWork w{reinterpret_cast<SplitItem*>(ws + L.split), reinterpret_cast<float2*>(ws + L.ml),
                     reinterpret_cast<float*>(ws + L.o)};
   CUtensorMap mk, mv, mq;
-  const int copy_keys = p.e4m3 ? 64 : c.keys;
-  if ((st = make_page_map(&mk, p, p.k, copy_keys)) != BSA_OK) return st;
-  if ((st = make_page_map(&mv, p, p.v, copy_keys)) != BSA_OK) return st;
-  if (c.rows == 16) return cuda_status(launch_paged_rows(mk, mv, p, w, c.grid, s));
+  // e4m3 V is converted on its way, 64 keys at a time; K is an operand as it lies
+  const bool tiles = c.rows != 16;
+  if ((st = make_page_map(&mk, p, p.k, c.keys, tiles && p.e4m3 && p.d == 64)) != BSA_OK) return st;
+  if ((st = make_page_map(&mv, p, p.v, p.e4m3 ? 64 : c.keys)) != BSA_OK) return st;
+  if (!tiles) return cuda_status(launch_paged_rows(mk, mv, p, w, c.grid, s));
   if ((st = make_map(&mq, Q, (long long)p.B * p.Hkv, p.G * p.N, p.d)) != BSA_OK) return st;
   return cuda_status(launch_paged_tiles(mq, mk, mv, p, w, c.rows, c.row_tiles, c.grid, s));
 }

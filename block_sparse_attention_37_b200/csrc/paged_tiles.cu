@@ -17,15 +17,20 @@
 //   warp 2      TMA producer of V; clears the rows of V no key owns
 //   warp 3      TMA producer of Q, ahead of the item's first product
 //   warps 4-11  the softmax warpgroups
-//   warps 12-15 (e4m3) converters: warp 0 then loads K and V as codes, and
-//               these four turn them into the fp16 tiles the products read
+//   warps 12-15 (e4m3) converters: warp 2 then loads V as codes, and these
+//               four turn them into the fp16 tiles that PV reads
 // Tensor memory: S at 128w with P written over it, O at 256 + Dw.
 //
-// e4m3: K's codes are exact in fp16, its scale multiplies the logits. V is
-// converted as code * scale / sigma (sigma a power of two, the largest V scale
-// of the piece so far), one rounding to fp16's 11 bits; O is rescaled when
-// sigma grows. Q is fp16 after a power-of-two scale of each row. The weights
-// are fp16 times 2^12: what is flushed is below 2^-36 of the largest.
+// e4m3: QK^T runs on K's codes as they are (kind::f8f6f4, twice the 16-bit
+// rate): each row of Q, scaled by a power of two, is the sum of two e4m3
+// values, its rounding and the rest, which hold bf16's eight bits exactly down
+// to 2^-9 of the row's largest value (2^-18 of it is the error below that), so
+// two products give the logits and take the time of one in bf16. K's scale
+// multiplies the logits. PV runs in fp16: V is code * scale / sigma (sigma a
+// power of two, the largest V scale of the piece so far) rounded once to 11
+// bits, the weights fp16 times 2^12 (what is flushed is below 2^-36 of the
+// largest); O is rescaled when sigma grows. Weights in e4m3 would lose those
+// below 2^-18, which a long context's sum needs.
 #include <type_traits>
 
 #include "mma_steps.cuh"
@@ -37,42 +42,68 @@ namespace bsa {
 constexpr int kTileKeys = 128;
 constexpr int kTilesMin = 4;  // a run is at least this many tiles
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool SPLIT>
 struct TilesCfg {
   static constexpr int THREADS = E4M3 ? 512 : 384;
-  static constexpr int S = D == 64 ? 4 : 2;        // K and V stages
-  static constexpr int TILE = 128 * D * 2;         // 16-bit tile of 128 rows
-  static constexpr int NCH = D / 64;
-  static constexpr int CHUNK = 128 * 128;
-  static constexpr int RAW = E4M3 ? 3 : 0;         // code pieces of 64 keys
+  static constexpr int CHUNK = 128 * 128;          // 128 rows of 128 bytes
+  static constexpr int QSLOTS = SPLIT ? 1 : 2;
+  static constexpr int QTILE = 128 * D * 2;        // bf16, or e4m3 twice
+  static constexpr int KTILE = 128 * D * (E4M3 ? 1 : 2);
+  static constexpr int VTILE = 128 * D * 2;
+  // Stages as shared memory allows. V's are held through a softmax, so where
+  // HBM is the bound (SPLIT) it gets the room of the second Q slot.
+  static constexpr int SK = D == 64 ? 4 : !E4M3 ? 2 : SPLIT ? 4 : 3;
+  static constexpr int SV = D == 64 ? (SPLIT ? 6 : 4) : SPLIT && !E4M3 ? 3 : 2;
+  static constexpr int RAW = !E4M3 ? 0 : D == 64 ? 8 : 5;  // V code pieces of 64 keys
   static constexpr int RAW_BYTES = 64 * D;
-  static constexpr int K_OFF = 2 * TILE;           // after the two Q slots
-  static constexpr int V_OFF = K_OFF + S * TILE;
-  static constexpr int RAW_OFF = V_OFF + S * TILE;
-  static constexpr int LAND_OFF = RAW_OFF + RAW * RAW_BYTES;            // [2][K, V][128] scales as loaded
-  static constexpr int KSC_OFF = LAND_OFF + (E4M3 ? 2 * 2 * 512 : 0);   // [2 S][128] K scales of a tile
-  static constexpr int SIG_OFF = KSC_OFF + (E4M3 ? 2 * S * 512 : 0);    // [2 S] sigma of a tile
-  static constexpr int ML_OFF = SIG_OFF + (E4M3 ? 64 : 0);              // [128] warpgroup 1's (m, l, factor) (SPLIT)
-  static constexpr int ZS_OFF = ML_OFF + 128 * 16;                      // [128] row factors (SPLIT, e4m3)
-  static constexpr int BAR_OFF = ZS_OFF + (E4M3 ? 512 : 0);
-  static constexpr int NBAR = 4 + 1 + 4 * S + 1 + 8 + 1 + 2 * RAW;
+  // Scale and sigma ring: an entry is written again only when the K tile SK + SV
+  // later is loaded, after the product of the tile SV later, before which the
+  // issuer flushes the PVs (and so outlives the softmaxes) of this one
+  static constexpr int R = E4M3 ? SK + SV : 0;
+  static constexpr int K_OFF = QSLOTS * QTILE;
+  static constexpr int V_OFF = K_OFF + SK * KTILE;
+  static constexpr int RAW_OFF = V_OFF + SV * VTILE;
+  static constexpr int XCH_OFF = RAW_OFF + RAW * RAW_BYTES;     // SPLIT: 32 channels of 128 rows, fp32
+  static constexpr int LAND_OFF = XCH_OFF + (SPLIT ? 128 * 32 * 4 : 0);  // [RAW][128] V scales as loaded
+  static constexpr int KSC_OFF = LAND_OFF + RAW * 512;          // [R][128] K scales
+  static constexpr int SIG_OFF = KSC_OFF + R * 512;             // [R] sigma of a tile
+  static constexpr int ML_OFF = SIG_OFF + (E4M3 ? 64 : 0);      // [128] warpgroup 1's (m, l, factor) (SPLIT)
+  static constexpr int ZS_OFF = ML_OFF + (SPLIT ? 128 * 16 : 0);  // [128] row factors (SPLIT, e4m3)
+  static constexpr int BAR_OFF = ZS_OFF + (SPLIT && E4M3 ? 512 : 0);
+  static constexpr int NBAR = 4 + 1 + 2 * SK + 2 * SV + 1 + 8 + 1 + 2 * RAW + 2 * R;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
   static constexpr int SMEM = MISC_OFF + 16 + sizeof(Run) + 16 * 8;
   static constexpr int ALLOC = SMEM + 1024;
   static_assert(ALLOC <= 227 * 1024, "smem budget");
-  // register split: the launch gives every thread REGS; the softmax
-  // warpgroups rise, the others drop
-  static constexpr int REGS = E4M3 ? 128 : 168;
-  static constexpr int REGS_CTL = E4M3 ? 48 : 56;
-  static constexpr int REGS_CNV = 64;
-  static constexpr int REGS_SMX = E4M3 ? 200 : 224;
-  static_assert(128 * REGS_CTL + 256 * REGS_SMX + (E4M3 ? 128 * REGS_CNV : 0) <= THREADS * REGS,
-                "register split exceeds the launch allocation");
+  static_assert(SV <= 8 && R <= 16, "two bits a V stage; sigma's room");
 };
 
 // Instruction descriptor for kind::f16 with fp16 A and B and fp32 D.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Shared-memory matrix descriptor of K-major rows of 64 bytes, 64-byte swizzle
+// (16-byte unit u of row r sits at u ^ ((r >> 1) & 3)).
+__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)1 << 16;          // leading offset (unused by swizzled K-major)
+  d |= (uint64_t)(512 >> 4) << 32; // eight rows
+  d |= (uint64_t)1 << 46;          // descriptor version for sm_100
+  d |= (uint64_t)4 << 61;          // SWIZZLE_64B
+  return d;
+}
+
+// S (+)= A K^T over D / 32 k-steps of 32 e4m3 values (K-major rows of D bytes).
+template <int KK>
+__device__ __forceinline__ void qk8_part(uint32_t s_tmem, uint64_t qd, uint64_t kd, uint32_t idesc, uint32_t acc) {
+  umma8_ss_at_warp<KK * 2, KK * 2>(s_tmem, qd, kd, idesc, KK > 0 ? 1u : acc);
+}
+template <int... KK>
+__device__ __forceinline__ void qk8_sum(uint32_t s_tmem, uint64_t qd, uint64_t kd, uint32_t idesc, uint32_t acc,
+                                        std::integer_sequence<int, KK...>) {
+  (qk8_part<KK>(s_tmem, qd, kd, idesc, acc), ...);
 }
 
 // Which warpgroups need key tile kt (absolute) of a piece, and how many of
@@ -117,12 +148,12 @@ __device__ __forceinline__ void mul2(float& x0, float& x1, float c0, float c1) {
 }
 
 template <int D, bool E4M3, bool SPLIT>
-__global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
+__global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
     paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const PagedParams p, const PagedWork wk,
                        int row_tiles) {
-  using C = TilesCfg<D, E4M3>;
-  constexpr int S = C::S, ROWS = SPLIT ? 128 : 256;
+  using C = TilesCfg<D, E4M3, SPLIT>;
+  constexpr int SK = C::SK, SV = C::SV, ROWS = SPLIT ? 128 : 256;
   constexpr float kTau = E4M3 ? 3.f : 8.f;    // the state moves when a row's maximum grows by more than 2^kTau
   constexpr float kGain = E4M3 ? 12.f : 0.f;  // log2 of what the weights are held times
   extern __shared__ uint8_t smem_raw[];
@@ -133,11 +164,11 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);  // [2]
   uint64_t* q_ready = q_full + 2;    // [2] e4m3: Q converted
   uint64_t* q_empty = q_ready + 2;   // every QK^T of the piece complete
-  uint64_t* k_full = q_empty + 1;    // [S]
-  uint64_t* k_empty = k_full + S;
-  uint64_t* v_full = k_empty + S;
-  uint64_t* v_empty = v_full + S;
-  uint64_t* v_land = v_empty + S;    // V of a tile with rows to clear
+  uint64_t* k_full = q_empty + 1;    // [SK]
+  uint64_t* k_empty = k_full + SK;
+  uint64_t* v_full = k_empty + SK;   // [SV]
+  uint64_t* v_empty = v_full + SV;
+  uint64_t* v_land = v_empty + SV;   // V of a tile with rows to clear
   uint64_t* s_full = v_land + 1;     // [2]
   uint64_t* p_full = s_full + 2;     // [2]
   uint64_t* o_ready = p_full + 2;    // [2]
@@ -145,6 +176,8 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
   uint64_t* mma_done = o_free + 2;
   uint64_t* raw_full = mma_done + 1; // [RAW]
   uint64_t* raw_empty = raw_full + C::RAW;
+  uint64_t* sc_full = raw_empty + C::RAW;  // [R] e4m3: K scales of a tile
+  uint64_t* sig_full = sc_full + C::R;     // [R] e4m3: sigma of a tile
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   Run* run_sh = reinterpret_cast<Run*>(smem + C::MISC_OFF + 16);
@@ -164,15 +197,21 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
     mbar_init(q_empty, 1);
     mbar_init(v_land, 1);
     mbar_init(mma_done, 1);
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&k_full[s], E4M3 ? 4 : 1);
-      mbar_init(&v_full[s], E4M3 ? 4 : 1);
+    for (int s = 0; s < SK; ++s) {
+      mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < SV; ++s) {
+      mbar_init(&v_full[s], E4M3 ? 4 : 1);
       mbar_init(&v_empty[s], 1);
     }
     for (int s = 0; s < C::RAW; ++s) {
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], 4);
+    }
+    for (int s = 0; s < C::R; ++s) {
+      mbar_init(&sc_full[s], 1);
+      mbar_init(&sig_full[s], 1);
     }
     misc[1] = 0;
     fence_barrier_init();
@@ -189,8 +228,6 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = misc[0];
 
-  // every role ends with its own copy of the teardown (a shared tail would
-  // make the register allocator apply the control warpgroup's limit to all)
   auto teardown = [&]() {
     tc_fence_before();
     __syncthreads();
@@ -205,7 +242,6 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
   const int page_mask = (1 << p.page_log2) - 1;
 
   if (warp < 4) {
-    regs_release<C::REGS_CTL>();
     if (warp == 3) {
       // ------------------------------------------------------------- Q producer
       int pc = 0;
@@ -222,23 +258,22 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
         }
         if (lane == 0)
           for (int w = 0; w < (SPLIT ? 1 : 2); ++w) {
-            mbar_arrive_expect_tx(&q_full[w], C::TILE);
-            for (int c = 0; c < C::NCH; ++c)
+            mbar_arrive_expect_tx(&q_full[w], C::QTILE);
+            for (int c = 0; c < D / 64; ++c)
               for (int h2 = 0; h2 < 2; ++h2)  // rows past the head's G N read as zeros
-                tma_load_3d(sQ + w * C::TILE + c * C::CHUNK + h2 * (C::CHUNK / 2), &tmQ, &q_full[w], c * 64,
+                tma_load_3d(sQ + w * C::QTILE + c * C::CHUNK + h2 * (C::CHUNK / 2), &tmQ, &q_full[w], c * 64,
                             q.rt * ROWS + 128 * w + 64 * h2, q.b * p.Hkv + q.hk);
           }
         __syncwarp();
       }
       if (*abort_flag && pc > 0 && lane == 0)
         for (int w = 0; w < (SPLIT ? 1 : 2); ++w) mbar_drain(&q_full[w], (uint32_t)(pc - 1) & 1u);
-    } else if (warp == 0 || (warp == 2 && !E4M3)) {
+    } else if (warp == 2 && E4M3) {
       if constexpr (E4M3) {
-        // ------------------------------------------------------- code producer
-        // pieces of 64 keys: K low, K high, V low, V high of every tile; the
-        // tile's scales land with the first
+        // ------------------------------------------------------- V code producer
+        // pieces of 64 keys; the tile's scales land with the first
         const int per = min(page_mask + 1, 64), sub = 64 / per;
-        const int part = lane & 3, role = lane >> 2;  // role 0: codes, 1..4: scales (K, V) x (low, high)
+        const int part = lane & 3, role = lane >> 2;  // role 0: codes, 1 and 2: scales of the low and high half
         int c = 0, k = 0;
         bool ok = true;
         while (run.left > 0 && ok) {
@@ -258,10 +293,10 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
             if (i + 1 < q.m) next = entry_of(kt + 1);
             if (need.mask(kt) == 0) continue;
             const int page = lane < 2 * sub && keeps(kt * kTileKeys + lane * per) ? checked_page(p, entry) : 0;
-            for (int x = 0; x < 4; ++x, ++c) {
-              const int half = role == 0 ? x & 1 : (role - 1) & 1;
+            for (int x = 0; x < 2; ++x, ++c) {
+              const int half = role == 0 ? x : (role - 1) & 1;
               const int j0 = kt * kTileKeys + 64 * half + part * per;
-              const bool mine = part < sub && keeps(j0) && (role == 0 || (x == 0 && role <= 4));
+              const bool mine = part < sub && keeps(j0) && (role == 0 || (x == 0 && role <= 2));
               const int pg = __shfl_sync(0xffffffffu, page, half * sub + part);
               const int st = c % C::RAW;
               if (c >= C::RAW) ok = wait(&raw_empty[st], c / C::RAW - 1);
@@ -269,18 +304,17 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
                 cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
                 break;
               }
-              if (k == p.withhold_tile && x == 0) continue;  // failure-detection test
               const uint32_t codes = __popc(__ballot_sync(0xffffffffu, mine && role == 0));
               const uint32_t scales = __popc(__ballot_sync(0xffffffffu, mine && role != 0));
               if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], codes * per * D + scales * per * 4);
               __syncwarp();
               if (mine) {
                 if (role == 0)
-                  tma_load_3d(smem + C::RAW_OFF + st * C::RAW_BYTES + part * per * D, x < 2 ? &tmK : &tmV, &raw_full[st],
-                              0, (j0 & page_mask) * D / 128, pg * p.Hkv + q.hk);
+                  tma_load_3d(smem + C::RAW_OFF + st * C::RAW_BYTES + part * per * D, &tmV, &raw_full[st], 0,
+                              (j0 & page_mask) * D / 128, pg * p.Hkv + q.hk);
                 else
-                  bulk_load_1d(smem + C::LAND_OFF + ((k & 1) * 2 + ((role - 1) >> 1)) * 512 + (64 * half + part * per) * 4,
-                               (role <= 2 ? p.k_scale : p.v_scale) + cache_row(p, pg, q.hk, j0), per * 4, &raw_full[st]);
+                  bulk_load_1d(smem + C::LAND_OFF + (k % C::RAW) * 512 + (64 * half + part * per) * 4,
+                               p.v_scale + cache_row(p, pg, q.hk, j0), per * 4, &raw_full[st]);
               }
               __syncwarp();
             }
@@ -288,86 +322,104 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
           }
         }
         if (*abort_flag && lane == 0)
-          for (int t = max(0, c - C::RAW); t < c; ++t)
-            if (t != 4 * p.withhold_tile) mbar_drain(&raw_full[t % C::RAW], (uint32_t)(t / C::RAW) & 1u);
-      } else {
-        // ------------------------------------------------------- K and V producers
-        auto produce = [&](auto ring) {
-          constexpr bool IS_K = decltype(ring)::value;
-          uint64_t* const full = IS_K ? k_full : v_full;
-          uint64_t* const empty = IS_K ? k_empty : v_empty;
-          const int per = min(page_mask + 1, kTileKeys), sub = kTileKeys / per;
-          const int part = lane / C::NCH, ch = lane % C::NCH;
-          int k = 0, landed = 0;
-          bool ok = true;
-          while (run.left > 0 && ok) {
-            const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
-            const TileNeed<SPLIT> need(p, q);
-            int j0 = (q.s.t0 + q.t) * kTileKeys + part * per;  // first token of this lane's copies
-            auto keeps = [&](int j) { return part < sub && j < q.s.hi && j + per > q.s.lo; };
-            int next = keeps(j0) ? table_entry(p, q.b, j0) : 0;
-            for (int i = 0; i < q.m; ++i, j0 += kTileKeys) {
-              const int kt = q.s.t0 + q.t + i;
-              const bool mine = keeps(j0);
-              const int entry = next;  // the next tile's is on its way while this one waits for its stage
-              next = i + 1 < q.m && keeps(j0 + kTileKeys) ? table_entry(p, q.b, j0 + kTileKeys) : 0;
-              if (need.mask(kt) == 0) continue;
-              const int st = k % S, key0 = kt * kTileKeys;
-              if (k >= S) ok = wait(&empty[st], k / S - 1);
+          for (int t = max(0, c - C::RAW); t < c; ++t) mbar_drain(&raw_full[t % C::RAW], (uint32_t)(t / C::RAW) & 1u);
+      }
+    } else if (warp == 0 || warp == 2) {
+      // --------------------------------------------------------- K and V producers
+      auto produce = [&](auto ring) {
+        constexpr bool IS_K = decltype(ring)::value;
+        constexpr int S = IS_K ? SK : SV;
+        constexpr int ROW = E4M3 ? D : 128;  // bytes of a token's row in one copy
+        uint64_t* const full = IS_K ? k_full : v_full;
+        uint64_t* const empty = IS_K ? k_empty : v_empty;
+        const int per = min(page_mask + 1, kTileKeys), sub = kTileKeys / per;
+        // a lane a copy: role = 64-channel half, or (e4m3) the K scales
+        const int part = lane & 7, role = lane >> 3;
+        const bool copies_tile = role < (E4M3 ? 1 : D / 64);
+        int k = 0, landed = 0;
+        bool ok = true;
+        while (run.left > 0 && ok) {
+          const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
+          const TileNeed<SPLIT> need(p, q);
+          int j0 = (q.s.t0 + q.t) * kTileKeys + part * per;  // first token of this lane's copies
+          auto keeps = [&](int j) { return part < sub && role < 2 && j < q.s.hi && j + per > q.s.lo; };
+          int next = keeps(j0) ? table_entry(p, q.b, j0) : 0;
+          for (int i = 0; i < q.m; ++i, j0 += kTileKeys) {
+            const int kt = q.s.t0 + q.t + i;
+            const bool mine = keeps(j0);
+            const int entry = next;  // the next tile's is on its way while this one waits for its stage
+            next = i + 1 < q.m && keeps(j0 + kTileKeys) ? table_entry(p, q.b, j0 + kTileKeys) : 0;
+            if (need.mask(kt) == 0) continue;
+            const int st = k % S, key0 = kt * kTileKeys;
+            if (k >= S) ok = wait(&empty[st], k / S - 1);
+            if (!ok) {
+              cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
+              break;
+            }
+            if (IS_K && k == p.withhold_tile) {  // failure-detection test
+              ++k;
+              continue;
+            }
+            // V rows of no kept key: their weights are zero, but whatever
+            // the slots hold (NaN, even) must not meet them
+            const bool clear = !IS_K && (key0 < q.s.lo || key0 + kTileKeys > q.s.hi);
+            uint64_t* bar = clear ? v_land : &full[st];
+            const uint32_t copies = __popc(__ballot_sync(0xffffffffu, mine && copies_tile));
+            if (lane == 0) {
+              mbar_arrive_expect_tx(bar, copies * per * ROW);
+              if constexpr (E4M3) mbar_arrive_expect_tx(&sc_full[k % C::R], copies * per * 4);
+            }
+            __syncwarp();
+            uint8_t* tile = IS_K ? sK + st * C::KTILE : sV + st * C::VTILE;
+            if (mine) {
+              const int pg = checked_page(p, entry);
+              if (copies_tile) {
+                tma_load_3d(tile + role * C::CHUNK + part * per * ROW, IS_K ? &tmK : &tmV, bar, role * 64,
+                            j0 & page_mask, pg * p.Hkv + q.hk);
+              } else if constexpr (E4M3) {
+                bulk_load_1d(smem + C::KSC_OFF + (k % C::R) * 512 + part * per * 4,
+                             p.k_scale + cache_row(p, pg, q.hk, j0), per * 4, &sc_full[k % C::R]);
+              }
+            }
+            __syncwarp();
+            if (clear) {
+              ok = wait(v_land, landed++);
               if (!ok) {
                 cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
+                if (lane == 0) mbar_drain(v_land, (uint32_t)(landed - 1) & 1u);
                 break;
               }
-              if (IS_K && k == p.withhold_tile) {  // failure-detection test
-                ++k;
-                continue;
+              const int a = max(q.s.lo - key0, 0), e = min(q.s.hi - key0, kTileKeys);  // rows [a, e) stay
+              constexpr int U = D / 8;  // 16-byte units of a row
+              for (int x = lane; x < (kTileKeys - (e - a)) * U; x += 32) {
+                const int u = x % U, r0 = x / U;
+                const int r = r0 < a ? r0 : r0 - a + e;
+                *reinterpret_cast<uint4*>(tile + (u >> 3) * C::CHUNK + r * 128 + (u & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
               }
-              // V rows of no kept key: their weights are zero, but whatever
-              // the slots hold (NaN, even) must not meet them
-              const bool clear = !IS_K && (key0 < q.s.lo || key0 + kTileKeys > q.s.hi);
-              uint64_t* bar = clear ? v_land : &full[st];
-              const uint32_t copies = __popc(__ballot_sync(0xffffffffu, mine));
-              if (lane == 0) mbar_arrive_expect_tx(bar, copies * per * 128);
+              fence_proxy_async_smem();
               __syncwarp();
-              uint8_t* tile = (IS_K ? sK : sV) + st * C::TILE;
-              if (mine)
-                tma_load_3d(tile + ch * C::CHUNK + part * per * 128, IS_K ? &tmK : &tmV, bar, ch * 64, j0 & page_mask,
-                            checked_page(p, entry) * p.Hkv + q.hk);
-              __syncwarp();
-              if (clear) {
-                ok = wait(v_land, landed++);
-                if (!ok) {
-                  cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
-                  if (lane == 0) mbar_drain(v_land, (uint32_t)(landed - 1) & 1u);
-                  break;
-                }
-                const int a = max(q.s.lo - key0, 0), e = min(q.s.hi - key0, kTileKeys);  // rows [a, e) stay
-                for (int x = lane; x < (kTileKeys - (e - a)) * 8 * C::NCH; x += 32) {
-                  const int u = x % (8 * C::NCH), r0 = x / (8 * C::NCH);
-                  const int r = r0 < a ? r0 : r0 - a + e;
-                  *reinterpret_cast<uint4*>(tile + (u >> 3) * C::CHUNK + r * 128 + (u & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[st]);
-              }
-              ++k;
+              if (lane == 0) mbar_arrive(&full[st]);
             }
+            ++k;
           }
-          // copies in flight land before the CTA ends; a stage whose tile was
-          // cleared by this warp has landed already
-          if (*abort_flag && lane == 0)
-            for (int t = max(0, k - S); t < k; ++t)
-              if (!IS_K || t != p.withhold_tile) mbar_drain(&full[t % S], (uint32_t)(t / S) & 1u);
-        };
-        if (warp == 0)
-          produce(std::true_type{});
-        else
-          produce(std::false_type{});
-      }
+        }
+        // copies in flight land before the CTA ends; a stage whose tile was
+        // cleared by this warp has landed already
+        if (*abort_flag && lane == 0) {
+          for (int t = max(0, k - S); t < k; ++t)
+            if (!IS_K || t != p.withhold_tile) mbar_drain(&full[t % S], (uint32_t)(t / S) & 1u);
+          if constexpr (E4M3)
+            for (int t = max(0, k - C::R); t < k; ++t)
+              if (t != p.withhold_tile) mbar_drain(&sc_full[t % C::R], (uint32_t)(t / C::R) & 1u);
+        }
+      };
+      if (warp == 0)
+        produce(std::true_type{});
+      else
+        produce(std::false_type{});
     } else if (warp == 1) {
       // ------------------------------------------------------------- MMA issuer
-      constexpr uint32_t idesc_qk = E4M3 ? idesc_f16_f32(128, 128, false) : idesc_bf16_f32(128, 128, false, false);
+      constexpr uint32_t idesc_qk = E4M3 ? idesc_e4m3_f32(128, 128) : idesc_bf16_f32(128, 128, false, false);
       constexpr uint32_t idesc_pv = E4M3 ? idesc_f16_f32(128, D, true) : idesc_bf16_f32(128, D, false, true);
       const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV);
       int pt0 = -1, pt1 = -1;    // tile whose PV is outstanding, per warpgroup
@@ -380,9 +432,9 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
       // V tiles are observed in tile order, so the parity test never meets
       // another phase of a shared stage
       auto pv = [&](int w) -> bool {
-        const int u = w ? pt1 : pt0, st = u % S;
+        const int u = w ? pt1 : pt0, st = u % SV;
         for (; v_seen <= u; ++v_seen)
-          if (!wait(&v_full[v_seen % S], v_seen / S)) return false;
+          if (!wait(&v_full[v_seen % SV], v_seen / SV)) return false;
         bool& fresh = w ? new1 : new0;
         if (fresh) {  // O of the piece before has been read
           int& nf = w ? nf1 : nf0;
@@ -393,7 +445,7 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
         if (!wait(&p_full[w], np)) return false;
         ++np;
         tc_fence_after();
-        pv_all(tmem + 256 + w * D, tmem + 128 * w, smem_desc_sw128(sVa + st * C::TILE, C::CHUNK, 1024), idesc_pv,
+        pv_all(tmem + 256 + w * D, tmem + 128 * w, smem_desc_sw128(sVa + st * C::VTILE, C::CHUNK, 1024), idesc_pv,
                fresh ? 1u : 0u, std::make_integer_sequence<int, 8>{});
         fresh = false;
         tc_commit_warp(&o_ready[w]);
@@ -410,8 +462,18 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
       };
       auto qk = [&](int w, int st) {
         tc_fence_after();
-        qk_all(tmem + 128 * w, smem_desc_sw128(sQa + (SPLIT ? 0 : w) * C::TILE, 16, 1024),
-               smem_desc_sw128(sKa + st * C::TILE, 16, 1024), idesc_qk, std::make_integer_sequence<int, D / 16>{});
+        const uint32_t qa = sQa + (SPLIT ? 0 : w) * C::QTILE, ka = sKa + st * C::KTILE;
+        if constexpr (!E4M3) {
+          qk_all(tmem + 128 * w, smem_desc_sw128(qa, 16, 1024), smem_desc_sw128(ka, 16, 1024), idesc_qk,
+                 std::make_integer_sequence<int, D / 16>{});
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)  // the row's rounding, then the rest
+            qk8_sum(tmem + 128 * w,
+                    D == 128 ? smem_desc_sw128(qa + h * 128 * D, 16, 1024) : smem_desc_sw64(qa + h * 128 * D),
+                    D == 128 ? smem_desc_sw128(ka, 16, 1024) : smem_desc_sw64(ka), idesc_qk, (uint32_t)h,
+                    std::make_integer_sequence<int, D / 32>{});
+        }
         tc_commit_warp(&s_full[w]);
         issued = true;
       };
@@ -423,10 +485,10 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
         for (int i = 0; i < q.m && ok; ++i) {
           const int nw = need.mask(q.s.t0 + q.t + i);
           if (nw == 0) continue;
-          const int st = k % S;
-          ok = wait(&k_full[st], k / S) && flush_below(k - S + 1);
+          const int st = k % SK;
+          ok = wait(&k_full[st], k / SK) && flush_below(k - SV + 1);
           if (!ok) break;
-          rem |= (uint32_t)__popc(nw) << (2 * st);
+          rem |= (uint32_t)__popc(nw) << (2 * (k % SV));
           if (nw & 1) {
             if (pt0 >= 0 && !(ok = pv(0))) break;
             qk(0, st);
@@ -453,7 +515,6 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
     }
     teardown();
   } else if (warp < 12) {
-    regs_claim<C::REGS_SMX>();
     // --------------------------------------------------------------- softmax
     const int w = (warp - 4) >> 2, q4 = warp & 3;
     const int r = q4 * 32 + lane;
@@ -484,35 +545,50 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
       float zs = p.scale_log2;
       if constexpr (E4M3) {
         if (!SPLIT || w == 0) {
-          // Q to fp16 in place, this thread's row after a power-of-two scale
-          // (exact down to 2^-24 of the row's largest value)
+          // this thread's row of Q in place as two e4m3 rows, after a power-of-
+          // two scale that leaves its largest value in [2^7, 2^8)
           ok = ok && wait(&q_full[w], pc);
-          if (ok) {
-            uint8_t* row = sQ + (SPLIT ? 0 : w) * C::TILE + r * 128;
-            uint32_t top = 0u;
+          uint8_t* base = sQ + (SPLIT ? 0 : w) * C::QTILE;
+          uint4 x[D / 8];
+          uint32_t top = 0u;
 #pragma unroll
-            for (int u = 0; u < D / 8; ++u) {
-              const uint4 x = *reinterpret_cast<const uint4*>(row + (u >> 3) * C::CHUNK + (((u ^ r) & 7) << 4));
-              const uint32_t y = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                          __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
-              top = max(top, max(y & 0xffffu, y >> 16));
-            }
-            const int ex = min(max((int)(top >> 7), 1), 253);
-            const float down = __int_as_float((254 - ex) << 23);
-            zs *= __int_as_float(ex << 23);
-#pragma unroll
-            for (int u = 0; u < D / 8; ++u) {
-              uint4* at4 = reinterpret_cast<uint4*>(row + (u >> 3) * C::CHUNK + (((u ^ r) & 7) << 4));
-              uint4 x = *at4;
-              auto half2 = [&](uint32_t v) {
-                return pack_f16x2(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xffff0000u) * down);
-              };
-              *at4 = make_uint4(half2(x.x), half2(x.y), half2(x.z), half2(x.w));
-            }
-            if constexpr (SPLIT) zs_sh[r] = zs;
-          } else {
-            cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
+          for (int u = 0; u < D / 8; ++u) {
+            x[u] = *reinterpret_cast<const uint4*>(base + (u >> 3) * C::CHUNK + r * 128 + (((u ^ r) & 7) << 4));
+            const uint32_t y = __vmaxu2(__vmaxu2(x[u].x & 0x7fff7fffu, x[u].y & 0x7fff7fffu),
+                                        __vmaxu2(x[u].z & 0x7fff7fffu, x[u].w & 0x7fff7fffu));
+            top = max(top, max(y & 0xffffu, y >> 16));
           }
+          // 2^(7 - e), e the exponent of the largest value, kept in the normal range
+          const int ex = min(max((int)(top >> 7), 8), 253);
+          const float down = __int_as_float((261 - ex) << 23);
+          zs *= top < 0x7f80u ? __int_as_float((ex - 7) << 23) : __int_as_float(0x7fc00000);  // a row with inf or NaN
+          named_bar(1 + w, 128);  // every row is read: at d = 64 the two forms lie elsewhere
+#pragma unroll
+          for (int u = 0; u < D / 16; ++u) {  // 16 values: a unit of each form
+            uint32_t hw[4], lw[4];
+            const uint32_t v[8] = {x[2 * u].x, x[2 * u].y, x[2 * u].z, x[2 * u].w,
+                                   x[2 * u + 1].x, x[2 * u + 1].y, x[2 * u + 1].z, x[2 * u + 1].w};
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              const float a = __uint_as_float(v[n] << 16) * down, b = __uint_as_float(v[n] & 0xffff0000u) * down;
+              const uint32_t hi = e4m3x2(a, b);
+              const uint32_t h2 = codes_lo(hi);
+              const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+              const uint32_t lo8 = e4m3x2(a - hf.x, b - hf.y);
+              if (n & 1) {
+                hw[n >> 1] |= hi << 16;
+                lw[n >> 1] |= lo8 << 16;
+              } else {
+                hw[n >> 1] = hi;
+                lw[n >> 1] = lo8;
+              }
+            }
+            const int off = D == 128 ? r * 128 + (((u ^ r) & 7) << 4) : r * 64 + (((u ^ (r >> 1)) & 3) << 4);
+            *reinterpret_cast<uint4*>(base + off) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+            *reinterpret_cast<uint4*>(base + 128 * D + off) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+          }
+          if constexpr (SPLIT) zs_sh[r] = zs;
+          if (!ok) cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
           fence_proxy_async_smem();
           mbar_arrive(&q_ready[w]);
         } else {
@@ -535,54 +611,63 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
         tc_fence_after();
         if (warp_rows) {
           const int key0 = kt * kTileKeys;
-          float sv[128];
-          tmem_ld32(stm, sv);
-          tmem_ld32(stm + 32, sv + 32);
-          tmem_ld32(stm + 64, sv + 64);
-          tmem_ld32(stm + 96, sv + 96);
-          tc_wait_ld();
-          float beta = 1.f;
+          const float4* ks = reinterpret_cast<const float4*>(smem + C::KSC_OFF + (E4M3 ? kk % C::R : 0) * 512);
           if constexpr (E4M3) {
-            const float4* ks = reinterpret_cast<const float4*>(smem + C::KSC_OFF + (kk % (2 * S)) * 512);
+            ok = wait(&sc_full[kk % C::R], kk / C::R);
+            if (!ok) break;
+          }
+          const bool edge = key0 < clo || key0 + kTileKeys > chi;
+          const int first = lo - key0, n = hi - lo;  // the row keeps columns [first, first + n)
+          // 32 scores of the row, masked. The row is read twice, for its
+          // maximum and for its weights, in loops that stay rolled: unrolled
+          // over a whole row in registers this code outgrew the instruction
+          // cache beside the other roles' and took twice the time (e4m3)
+          auto scores = [&](int c, float (&x)[32]) {
+            tmem_ld32(stm + 32 * c, x);
+            tc_wait_ld();
+            if constexpr (E4M3) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const float4 s4 = ks[c];
-              mul2(sv[4 * c], sv[4 * c + 1], s4.x, s4.y);
-              mul2(sv[4 * c + 2], sv[4 * c + 3], s4.z, s4.w);
+              for (int e = 0; e < 8; ++e) {
+                const float4 s4 = ks[8 * c + e];
+                mul2(x[4 * e], x[4 * e + 1], s4.x, s4.y);
+                mul2(x[4 * e + 2], x[4 * e + 3], s4.z, s4.w);
+              }
             }
-            const float now = *reinterpret_cast<const float*>(smem + C::SIG_OFF + (kk % (2 * S)) * 4);
-            if (jp > 0) beta = sig / now;  // both powers of two
-            sig = now;
-          }
-          if (key0 < clo || key0 + kTileKeys > chi) {
-            const int a = lo - key0, n = hi - lo;
+            if (edge) {
 #pragma unroll
-            for (int c = 0; c < 128; ++c) sv[c] = (uint32_t)(c - a) < (uint32_t)n ? sv[c] : kNegInf;
-          }
-          float x0 = max3f(sv[0], sv[1], sv[2]), x1 = max3f(sv[3], sv[4], sv[5]);
-          float x2 = max3f(sv[64], sv[65], sv[66]), x3 = max3f(sv[67], sv[68], sv[69]);
+              for (int e = 0; e < 32; ++e) x[e] = (uint32_t)(32 * c + e - first) < (uint32_t)n ? x[e] : kNegInf;
+            }
+          };
+          float top = kNegInf;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float x[32];
+            scores(c, x);
+            float t0 = max3f(x[0], x[1], x[2]), t1 = max3f(x[3], x[4], x[5]);
 #pragma unroll
-          for (int c = 6; c < 62; c += 4) {
-            x0 = max3f(x0, sv[c], sv[c + 1]);
-            x1 = max3f(x1, sv[c + 2], sv[c + 3]);
-            x2 = max3f(x2, sv[64 + c], sv[65 + c]);
-            x3 = max3f(x3, sv[66 + c], sv[67 + c]);
+            for (int e = 6; e < 30; e += 4) {
+              t0 = max3f(t0, x[e], x[e + 1]);
+              t1 = max3f(t1, x[e + 2], x[e + 3]);
+            }
+            top = max3f(max3f(t0, x[30], x[31]), t1, top);
           }
-          const float top = max3f(max3f(x0, x1, x2), x3, max3f(sv[62], sv[63], fmaxf(sv[126], sv[127]))) * zs;
+          top *= zs;
           float alpha = 1.f;
           if (top > m + kTau) {
             alpha = fast_exp2(m - top);
             m = top;
           }
           const float off = kGain - (m == kNegInf ? 0.f : m);
-          // P over S, chunk by chunk: S(j) landing implies PV(j-1) is complete
+          // P over S, 16 columns behind every 32 read: S(j) landing implies PV(j-1) is complete
           float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
+            float x[32];
+            scores(c, x);
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float a = sv[32 * c + 2 * e], b = sv[32 * c + 2 * e + 1];
+              float a = x[2 * e], b = x[2 * e + 1];
               fma2(a, b, zs, off);
               a = fast_exp2(a);
               b = fast_exp2(b);
@@ -592,7 +677,13 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
             tmem_st16(stm + 16 * c, pk);
           }
           l = l * alpha + (sum0 + sum1);
-          alpha *= beta;
+          if constexpr (E4M3) {
+            ok = wait(&sig_full[kk % C::R], kk / C::R);
+            if (!ok) break;
+            const float now = *reinterpret_cast<const float*>(smem + C::SIG_OFF + (kk % C::R) * 4);
+            if (jp > 0) alpha *= sig / now;  // both powers of two
+            sig = now;
+          }
           if (jp > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
@@ -652,26 +743,22 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
       const float unit = E4M3 ? sig * (1.f / 128.f) : 1.f;  // what O is held over
       auto inverse = [&](float x) { return !whole ? 1.f : x > 0.f ? 1.f / x : x == 0.f ? 0.f : x; };
       if constexpr (SPLIT) {
-        // warpgroup 1 hands its half over through the unused Q slot, half of
-        // the channels at a time
-        float4* xch = reinterpret_cast<float4*>(sQ + C::TILE);
+        // warpgroup 1 hands its half over, 32 channels at a time
+        float4* xch = reinterpret_cast<float4*>(smem + C::XCH_OFF);
         float f0 = 0.f, f1 = 0.f;
         if (w == 1) ml_sh[r] = make_float4(m, l, unit, 0.f);
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          load(c, o);
           if (w == 1) {
-#pragma unroll 1
-            for (int c = 0; c < D / 64; ++c) {
-              float o[32];
-              load(h * (D / 64) + c, o);
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                xch[(c * 8 + e) * 128 + r] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            }
+            for (int e = 0; e < 8; ++e)
+              xch[e * 128 + r] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
           named_bar(3, 256);
           if (w == 0) {
-            if (h == 0) {
+            if (c == 0) {
               const float4 x = ml_sh[r];
               const float M = fmaxf(m, x.x), mu = M == kNegInf ? 0.f : M;
               const float e0 = fast_exp2(m - mu), e1 = fast_exp2(x.x - mu);
@@ -680,20 +767,15 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
               f0 = e0 * unit * inverse(l);
               f1 = e1 * x.z * inverse(l);
             }
-#pragma unroll 1
-            for (int c = 0; c < D / 64; ++c) {
-              float o[32];
-              load(h * (D / 64) + c, o);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 x = xch[(c * 8 + e) * 128 + r];
-                o[4 * e] = o[4 * e] * f0 + x.x * f1;
-                o[4 * e + 1] = o[4 * e + 1] * f0 + x.y * f1;
-                o[4 * e + 2] = o[4 * e + 2] * f0 + x.z * f1;
-                o[4 * e + 3] = o[4 * e + 3] * f0 + x.w * f1;
-              }
-              store(h * (D / 64) + c, o, 1.f);
+            for (int e = 0; e < 8; ++e) {
+              const float4 x = xch[e * 128 + r];
+              o[4 * e] = o[4 * e] * f0 + x.x * f1;
+              o[4 * e + 1] = o[4 * e + 1] * f0 + x.y * f1;
+              o[4 * e + 2] = o[4 * e + 2] * f0 + x.z * f1;
+              o[4 * e + 3] = o[4 * e + 3] * f0 + x.w * f1;
             }
+            store(c, o, 1.f);
           }
           named_bar(3, 256);
         }
@@ -716,7 +798,6 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
     teardown();
   } else {
     if constexpr (E4M3) {
-      regs_release<C::REGS_CNV>();
       // ------------------------------------------------------------- converters
       const int cw = warp - 12;
       int c = 0, k = 0;
@@ -728,23 +809,15 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
         for (int i = 0; i < q.m && ok; ++i) {
           const int kt = q.s.t0 + q.t + i;
           if (need.mask(kt) == 0) continue;
-          const int st = k % S, key0 = kt * kTileKeys;
+          const int st = k % SV, key0 = kt * kTileKeys;
           const bool edge = key0 < q.s.lo || key0 + kTileKeys > q.s.hi;
-          const float* land = reinterpret_cast<const float*>(smem + C::LAND_OFF + (k & 1) * 1024);
-          for (int x = 0; x < 4; ++x, ++c) {
-            const int half = x & 1;
-            const bool is_v = x >= 2;
+          const float* land = reinterpret_cast<const float*>(smem + C::LAND_OFF + (k % C::RAW) * 512);
+          for (int half = 0; half < 2; ++half, ++c) {
             ok = wait(&raw_full[c % C::RAW], c / C::RAW);
-            if (ok && half == 0 && k >= S) ok = wait(is_v ? &v_empty[st] : &k_empty[st], k / S - 1);
-            if (!ok) {
-              cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
-              break;
-            }
-            if (x == 0) {
-              // sigma from the tile's V scales (every warp finds the same),
-              // and K's scales into the ring that lives until the tile's PVs
+            if (ok && half == 0) {
+              // sigma from the tile's V scales; every warp finds the same
               const int j4 = key0 + 4 * lane;
-              const float4 f = reinterpret_cast<const float4*>(land + 128)[lane];
+              const float4 f = reinterpret_cast<const float4*>(land)[lane];
               const float fs[4] = {f.x, f.y, f.z, f.w};
               uint32_t top = 0u;
 #pragma unroll
@@ -754,11 +827,18 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
               }
               top = __reduce_max_sync(0xffffffffu, top);
               if (top > __float_as_uint(sig)) sig = __uint_as_float(min((top + 0x7fffffu) & 0x7f800000u, 0x7f000000u));
-              reinterpret_cast<float*>(smem + C::KSC_OFF + (k % (2 * S)) * 512)[32 * cw + lane] = land[32 * cw + lane];
-              if (cw == 0 && lane == 0) *reinterpret_cast<float*>(smem + C::SIG_OFF + (k % (2 * S)) * 4) = sig;
+              if (cw == 0 && lane == 0) {
+                *reinterpret_cast<float*>(smem + C::SIG_OFF + (k % C::R) * 4) = sig;
+                mbar_arrive(&sig_full[k % C::R]);
+              }
+              if (k >= SV) ok = wait(&v_empty[st], k / SV - 1);
+            }
+            if (!ok) {
+              cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
+              break;
             }
             const uint8_t* raw = smem + C::RAW_OFF + (c % C::RAW) * C::RAW_BYTES;
-            uint8_t* tile = (is_v ? sV : sK) + st * C::TILE;
+            uint8_t* tile = sV + st * C::VTILE;
             constexpr int UNITS = D / 16;                  // 16-code units of a token
             constexpr int STEP = 128 / UNITS;              // tokens a step of the warpgroup covers
             const int u = lane % UNITS;
@@ -767,19 +847,18 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
             for (int e = 0; e < 64 / STEP; ++e) {
               const int key = e * STEP + cw * (32 / UNITS) + lane / UNITS;  // of the piece
               const uint32_t lin = key * D + u * 16;
-              uint4 y = *reinterpret_cast<const uint4*>(raw + (lin ^ ((lin >> 3) & 0x70u)));
+              const uint4 y = *reinterpret_cast<const uint4*>(raw + (lin ^ ((lin >> 3) & 0x70u)));
               uint32_t h[8] = {codes_lo(y.x), codes_hi(y.x), codes_lo(y.y), codes_hi(y.y),
                                codes_lo(y.z), codes_hi(y.z), codes_lo(y.w), codes_hi(y.w)};
               const int row = 64 * half + key;
-              if (is_v) {
-                const float s = land[128 + row] * up;
-                const uint32_t s2 = pack_f16x2(s, s);
-                const bool out = edge && (key0 + row < q.s.lo || key0 + row >= q.s.hi);
+              const float s = land[row] * up;
+              const uint32_t s2 = pack_f16x2(s, s);
+              // rows of no kept key are cleared: their codes and scales may be anything
+              const bool out = edge && (key0 + row < q.s.lo || key0 + row >= q.s.hi);
 #pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                  const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&h[n]), *reinterpret_cast<const __half2*>(&s2));
-                  h[n] = out ? 0u : *reinterpret_cast<const uint32_t*>(&z);
-                }
+              for (int n = 0; n < 8; ++n) {
+                const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&h[n]), *reinterpret_cast<const __half2*>(&s2));
+                h[n] = out ? 0u : *reinterpret_cast<const uint32_t*>(&z);
               }
               uint8_t* dst = tile + (u >> 2) * C::CHUNK + row * 128;
               const int a = 2 * (u & 3);
@@ -790,7 +869,7 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3>::THREADS, 1)
             __syncwarp();
             if (lane == 0) {
               mbar_arrive(&raw_empty[c % C::RAW]);
-              if (half == 1) mbar_arrive(is_v ? &v_full[st] : &k_full[st]);
+              if (half == 1) mbar_arrive(&v_full[st]);
             }
           }
           ++k;
@@ -842,16 +921,10 @@ template <int D, bool E4M3, bool SPLIT>
 static cudaError_t launch_tiles_d(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                                   const PagedParams& p, const PagedWork& w, int row_tiles, int grid,
                                   cudaStream_t stream) {
-  using C = TilesCfg<D, E4M3>;
+  using C = TilesCfg<D, E4M3, SPLIT>;
   auto fn = paged_tiles_kernel<D, E4M3, SPLIT>;
   static DeviceOnce once;
   cudaError_t e = once.run([&]() -> cudaError_t {
-    // the register split needs the full launch allocation: a smaller one
-    // would leave setmaxnreg.inc waiting, so refuse to launch instead
-    cudaFuncAttributes fa;
-    cudaError_t r = cudaFuncGetAttributes(&fa, fn);
-    if (r != cudaSuccess) return r;
-    if (fa.numRegs != C::REGS) return cudaErrorInvalidKernelImage;
     return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
   });
   if (e != cudaSuccess) return e;
