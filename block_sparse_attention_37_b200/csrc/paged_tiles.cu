@@ -2,22 +2,23 @@
 // chunks of a prompt, blocks of tokens denoised together.
 //
 // Persistent CTAs, one an SM, each walk one run of the line of 128-key tiles
-// (paged_sched.cuh). An item is 256 query rows: two 128-row tiles, one a
-// softmax warpgroup, that share every K and V tile (a causal chunk's upper
-// tile skips the keys only the lower one keeps). With at most 128 rows
-// (SPLIT) both warpgroups hold the same rows and take alternate tiles; their
-// results are joined in the CTA, so the pipe still has two independent
-// softmaxes to work between. Either way the tensor core runs one warpgroup's
-// PV and next QK^T under the other's softmax, and the exponentials (16 a
-// clock and SM, 2048 clocks for a tile of 256 rows) and the products (as many)
-// bound a long chunk; K and V of a short one are bound by HBM.
+// (paged_sched.cuh). An item is 256 query rows: two 128-row tiles that share
+// every K and V tile (a causal chunk's upper tile skips the keys only the
+// lower one keeps). With at most 128 rows (SPLIT) both hold the same rows and
+// take alternate key tiles; their results are joined in the CTA, so the
+// tensor core still has two independent softmaxes to work between. Either way
+// it runs one row tile's PV and next QK^T under the other's softmax. A row
+// tile's softmax is two warpgroups, each half of the columns: a tile's chain
+// QK^T - softmax - PV is what a row tile waits for, and eight warps pass
+// through it in half the time of four.
 // Roles:
 //   warp 0      TMA producer of K (a lane a copy: a page's part of a tile)
 //   warp 1      TMEM allocator and tcgen05.mma issuer
 //   warp 2      TMA producer of V; clears the rows of V no key owns
 //   warp 3      TMA producer of Q, ahead of the item's first product
-//   warps 4-11  the softmax warpgroups
-//   warps 12-15 (e4m3) converters: warp 2 then loads V as codes, and these
+//   warps 4-19  the softmax warpgroups: row tile 0, columns 0-63 and 64-127,
+//               then row tile 1
+//   warps 20-23 (e4m3) converters: warp 2 then loads V as codes, and these
 //               four turn them into the fp16 tiles that PV reads
 // Tensor memory: S at 128w with P written over it, O at 256 + Dw.
 //
@@ -44,7 +45,7 @@ constexpr int kTilesMin = 4;  // a run is at least this many tiles
 
 template <int D, bool E4M3, bool SPLIT>
 struct TilesCfg {
-  static constexpr int THREADS = E4M3 ? 512 : 384;
+  static constexpr int THREADS = E4M3 ? 768 : 640;
   static constexpr int CHUNK = 128 * 128;          // 128 rows of 128 bytes
   static constexpr int QSLOTS = SPLIT ? 1 : 2;
   static constexpr int QTILE = 128 * D * 2;        // bf16, or e4m3 twice
@@ -54,7 +55,7 @@ struct TilesCfg {
   // HBM is the bound (SPLIT) it gets the room of the second Q slot.
   static constexpr int SK = D == 64 ? 4 : !E4M3 ? 2 : SPLIT ? 4 : 3;
   static constexpr int SV = D == 64 ? (SPLIT ? 6 : 4) : SPLIT && !E4M3 ? 3 : 2;
-  static constexpr int RAW = !E4M3 ? 0 : D == 64 ? 8 : 5;  // V code pieces of 64 keys
+  static constexpr int RAW = !E4M3 ? 0 : D == 64 ? 8 : 4;  // V code pieces of 64 keys
   static constexpr int RAW_BYTES = 64 * D;
   // Scale and sigma ring: an entry is written again only when the K tile SK + SV
   // later is loaded, after the product of the tile SV later, before which the
@@ -63,16 +64,17 @@ struct TilesCfg {
   static constexpr int K_OFF = QSLOTS * QTILE;
   static constexpr int V_OFF = K_OFF + SK * KTILE;
   static constexpr int RAW_OFF = V_OFF + SV * VTILE;
-  static constexpr int XCH_OFF = RAW_OFF + RAW * RAW_BYTES;     // SPLIT: 32 channels of 128 rows, fp32
+  static constexpr int XCH_OFF = RAW_OFF + RAW * RAW_BYTES;     // SPLIT: 2 x 16 channels of 128 rows, fp32
   static constexpr int LAND_OFF = XCH_OFF + (SPLIT ? 128 * 32 * 4 : 0);  // [RAW][128] V scales as loaded
   static constexpr int KSC_OFF = LAND_OFF + RAW * 512;          // [R][128] K scales
   static constexpr int SIG_OFF = KSC_OFF + R * 512;             // [R] sigma of a tile
-  static constexpr int ML_OFF = SIG_OFF + (E4M3 ? 64 : 0);      // [128] warpgroup 1's (m, l, factor) (SPLIT)
+  static constexpr int ML_OFF = SIG_OFF + (E4M3 ? 64 : 0);      // [128] row tile 1's (m, l, factor) (SPLIT)
   static constexpr int ZS_OFF = ML_OFF + (SPLIT ? 128 * 16 : 0);  // [128] row factors (SPLIT, e4m3)
-  static constexpr int BAR_OFF = ZS_OFF + (SPLIT && E4M3 ? 512 : 0);
+  static constexpr int MX_OFF = ZS_OFF + (SPLIT && E4M3 ? 512 : 0);  // [2][2][128] exchange of a row's two halves
+  static constexpr int BAR_OFF = MX_OFF + 4 * 128 * 4;
   static constexpr int NBAR = 4 + 1 + 2 * SK + 2 * SV + 1 + 8 + 1 + 2 * RAW + 2 * R;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
-  static constexpr int SMEM = MISC_OFF + 16 + sizeof(Run) + 16 * 8;
+  static constexpr int SMEM = MISC_OFF + 16 + sizeof(Run) + 24 * 8;
   static constexpr int ALLOC = SMEM + 1024;
   static_assert(ALLOC <= 227 * 1024, "smem budget");
   static_assert(SV <= 8 && R <= 16, "two bits a V stage; sigma's room");
@@ -106,11 +108,25 @@ __device__ __forceinline__ void qk8_sum(uint32_t s_tmem, uint64_t qd, uint64_t k
   (qk8_part<KK>(s_tmem, qd, kd, idesc, acc), ...);
 }
 
-// Which warpgroups need key tile kt (absolute) of a piece, and how many of
-// the piece's tiles each needs. Every role asks the same questions.
+// O (+)= P V over 8 k-steps of 16 keys, the weights of keys 0-63 in columns
+// 0-31 of S's place and those of keys 64-127 in columns 64-95.
+template <int KK>
+__device__ __forceinline__ void pv_half_step(uint32_t o_tmem, uint32_t p_tmem, uint64_t vd, uint32_t idesc,
+                                             uint32_t first) {
+  umma_ts_at_warp<(KK >> 2) * 64 + (KK & 3) * 8, KK * 2048 / 16>(o_tmem, p_tmem, vd, idesc,
+                                                                  (KK > 0 || !first) ? 1u : 0u);
+}
+template <int... KK>
+__device__ __forceinline__ void pv_halves(uint32_t o_tmem, uint32_t p_tmem, uint64_t vd, uint32_t idesc,
+                                          uint32_t first, std::integer_sequence<int, KK...>) {
+  (pv_half_step<KK>(o_tmem, p_tmem, vd, idesc, first), ...);
+}
+
+// Which row tiles need key tile kt (absolute) of a piece, and whether one needs
+// any. Every role asks the same questions.
 template <bool SPLIT>
 struct TileNeed {
-  int a0, e0, a1, e1;  // tile ranges of the warpgroups
+  int a0, e0, a1, e1;  // tile ranges of the row tiles
   int first;           // the piece's first tile (SPLIT)
   __device__ __forceinline__ TileNeed(const PagedParams& p, const Piece& q) {
     first = q.s.t0 + q.t;
@@ -188,11 +204,11 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
   if (tid == 0) {
     for (int w = 0; w < 2; ++w) {
       mbar_init(&q_full[w], 1);
-      mbar_init(&q_ready[w], 128);
+      mbar_init(&q_ready[w], 256);
       mbar_init(&s_full[w], 1);
-      mbar_init(&p_full[w], 128);
+      mbar_init(&p_full[w], 256);
       mbar_init(&o_ready[w], 1);
-      mbar_init(&o_free[w], 128);
+      mbar_init(&o_free[w], 256);
     }
     mbar_init(q_empty, 1);
     mbar_init(v_land, 1);
@@ -422,12 +438,12 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
       constexpr uint32_t idesc_qk = E4M3 ? idesc_e4m3_f32(128, 128) : idesc_bf16_f32(128, 128, false, false);
       constexpr uint32_t idesc_pv = E4M3 ? idesc_f16_f32(128, D, true) : idesc_bf16_f32(128, D, false, true);
       const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV);
-      int pt0 = -1, pt1 = -1;    // tile whose PV is outstanding, per warpgroup
+      int pt0 = -1, pt1 = -1;    // tile whose PV is outstanding, per row tile
       int np0 = 0, np1 = 0;      // PVs issued
       int nf0 = 0, nf1 = 0;      // pieces begun
       bool new0 = false, new1 = false;  // the next PV is the piece's first
       int v_seen = 0, k = 0, pc = 0;
-      uint32_t rem = 0u;         // warpgroups still to use a stage's V, two bits a stage
+      uint32_t rem = 0u;         // row tiles still to use a stage's V, two bits a stage
       bool ok = true, issued = false;
       // V tiles are observed in tile order, so the parity test never meets
       // another phase of a shared stage
@@ -445,8 +461,8 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
         if (!wait(&p_full[w], np)) return false;
         ++np;
         tc_fence_after();
-        pv_all(tmem + 256 + w * D, tmem + 128 * w, smem_desc_sw128(sVa + st * C::VTILE, C::CHUNK, 1024), idesc_pv,
-               fresh ? 1u : 0u, std::make_integer_sequence<int, 8>{});
+        pv_halves(tmem + 256 + w * D, tmem + 128 * w, smem_desc_sw128(sVa + st * C::VTILE, C::CHUNK, 1024), idesc_pv,
+                  fresh ? 1u : 0u, std::make_integer_sequence<int, 8>{});
         fresh = false;
         tc_commit_warp(&o_ready[w]);
         rem -= 1u << (2 * st);
@@ -514,16 +530,20 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
       }
     }
     teardown();
-  } else if (warp < 12) {
+  } else if (warp < 20) {
     // --------------------------------------------------------------- softmax
-    const int w = (warp - 4) >> 2, q4 = warp & 3;
+    const int w = (warp - 4) >> 3, hf = ((warp - 4) >> 2) & 1, q4 = warp & 3;
     const int r = q4 * 32 + lane;
+    const int pair_bar = 4 + 4 * w + q4;  // this warp and the one with the rows' other columns
+    const int kc = 64 * hf, oc = D / 2 * hf;  // first of this thread's columns of S, of O
+    float* mx_mine = reinterpret_cast<float*>(smem + C::MX_OFF) + (2 * w + hf) * 128 + r;
+    const float* mx_other = reinterpret_cast<float*>(smem + C::MX_OFF) + (2 * w + 1 - hf) * 128 + r;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const uint32_t stm = tmem + lane_off + 128 * w, otm = tmem + lane_off + 256 + w * D;
     const int slot_row = (SPLIT ? 0 : 128 * w) + r;  // row of the item
     float4* ml_sh = reinterpret_cast<float4*>(smem + C::ML_OFF);
     float* zs_sh = reinterpret_cast<float*>(smem + C::ZS_OFF);
-    int j = 0, k = 0, pc = 0;  // tiles of this warpgroup, tiles and pieces of the CTA
+    int j = 0, k = 0, pc = 0;  // tiles of this row tile, tiles and pieces of the CTA
     bool ok = true;
     SplitItem split{0, 0, 0, 0};
     for (; run.left > 0; ++pc) {
@@ -545,36 +565,41 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
       float zs = p.scale_log2;
       if constexpr (E4M3) {
         if (!SPLIT || w == 0) {
-          // this thread's row of Q in place as two e4m3 rows, after a power-of-
-          // two scale that leaves its largest value in [2^7, 2^8)
+          // this thread's half row of Q in place as two e4m3 parts, after a
+          // power-of-two scale that leaves the row's largest value in [2^7, 2^8)
           ok = ok && wait(&q_full[w], pc);
           uint8_t* base = sQ + (SPLIT ? 0 : w) * C::QTILE;
-          uint4 x[D / 8];
+          constexpr int U = D / 16;  // 16-byte units of the half row
+          uint4 x[U];
           uint32_t top = 0u;
 #pragma unroll
-          for (int u = 0; u < D / 8; ++u) {
-            x[u] = *reinterpret_cast<const uint4*>(base + (u >> 3) * C::CHUNK + r * 128 + (((u ^ r) & 7) << 4));
-            const uint32_t y = __vmaxu2(__vmaxu2(x[u].x & 0x7fff7fffu, x[u].y & 0x7fff7fffu),
-                                        __vmaxu2(x[u].z & 0x7fff7fffu, x[u].w & 0x7fff7fffu));
+          for (int e = 0; e < U; ++e) {
+            const int u = U * hf + e;
+            x[e] = *reinterpret_cast<const uint4*>(base + (u >> 3) * C::CHUNK + r * 128 + (((u ^ r) & 7) << 4));
+            const uint32_t y = __vmaxu2(__vmaxu2(x[e].x & 0x7fff7fffu, x[e].y & 0x7fff7fffu),
+                                        __vmaxu2(x[e].z & 0x7fff7fffu, x[e].w & 0x7fff7fffu));
             top = max(top, max(y & 0xffffu, y >> 16));
           }
+          *mx_mine = __uint_as_float(top);
+          named_bar(1 + w, 256);  // every row is read: at d = 64 the two forms lie elsewhere
+          top = max(top, __float_as_uint(*mx_other));
           // 2^(7 - e), e the exponent of the largest value, kept in the normal range
           const int ex = min(max((int)(top >> 7), 8), 253);
           const float down = __int_as_float((261 - ex) << 23);
           zs *= top < 0x7f80u ? __int_as_float((ex - 7) << 23) : __int_as_float(0x7fc00000);  // a row with inf or NaN
-          named_bar(1 + w, 128);  // every row is read: at d = 64 the two forms lie elsewhere
 #pragma unroll
-          for (int u = 0; u < D / 16; ++u) {  // 16 values: a unit of each form
+          for (int e = 0; e < U / 2; ++e) {  // 16 values: a unit of each form
+            const int u = U / 2 * hf + e;
             uint32_t hw[4], lw[4];
-            const uint32_t v[8] = {x[2 * u].x, x[2 * u].y, x[2 * u].z, x[2 * u].w,
-                                   x[2 * u + 1].x, x[2 * u + 1].y, x[2 * u + 1].z, x[2 * u + 1].w};
+            const uint32_t v[8] = {x[2 * e].x, x[2 * e].y, x[2 * e].z, x[2 * e].w,
+                                   x[2 * e + 1].x, x[2 * e + 1].y, x[2 * e + 1].z, x[2 * e + 1].w};
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
               const float a = __uint_as_float(v[n] << 16) * down, b = __uint_as_float(v[n] & 0xffff0000u) * down;
               const uint32_t hi = e4m3x2(a, b);
               const uint32_t h2 = codes_lo(hi);
-              const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-              const uint32_t lo8 = e4m3x2(a - hf.x, b - hf.y);
+              const float2 hf2 = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+              const uint32_t lo8 = e4m3x2(a - hf2.x, b - hf2.y);
               if (n & 1) {
                 hw[n >> 1] |= hi << 16;
                 lw[n >> 1] |= lo8 << 16;
@@ -587,60 +612,59 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
             *reinterpret_cast<uint4*>(base + off) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
             *reinterpret_cast<uint4*>(base + 128 * D + off) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
           }
-          if constexpr (SPLIT) zs_sh[r] = zs;
+          if constexpr (SPLIT)
+            if (hf == 0) zs_sh[r] = zs;
           if (!ok) cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
           fence_proxy_async_smem();
           mbar_arrive(&q_ready[w]);
         } else {
-          // the other warpgroup converts; it cannot pass this piece's join
+          // row tile 0's warpgroups convert; they cannot pass this piece's join
           // before this one
           ok = ok && wait(&q_ready[0], pc);
           zs = zs_sh[r];
         }
       }
       float m = kNegInf, l = 0.f, sig = 1.f;
-      int jp = 0;  // tiles of this warpgroup in the piece
-      for (int i = 0; i < q.m && ok; ++i) {
+      int jp = 0;  // tiles of this row tile in the piece
+      // An aborting CTA walks its tiles without waiting or computing: a row's
+      // two warps meet in a barrier every tile, so neither may leave early.
+      for (int i = 0; i < q.m; ++i) {
         const int kt = q.s.t0 + q.t + i;
         const int nw = need.mask(kt);
         if (nw == 0) continue;
         const int kk = k++;
         if (!((nw >> w) & 1)) continue;
-        ok = wait(&s_full[w], j);
-        if (!ok) break;
+        ok = ok && wait(&s_full[w], j);
         tc_fence_after();
         if (warp_rows) {
           const int key0 = kt * kTileKeys;
           const float4* ks = reinterpret_cast<const float4*>(smem + C::KSC_OFF + (E4M3 ? kk % C::R : 0) * 512);
-          if constexpr (E4M3) {
-            ok = wait(&sc_full[kk % C::R], kk / C::R);
-            if (!ok) break;
-          }
+          if constexpr (E4M3) ok = ok && wait(&sc_full[kk % C::R], kk / C::R);
           const bool edge = key0 < clo || key0 + kTileKeys > chi;
           const int first = lo - key0, n = hi - lo;  // the row keeps columns [first, first + n)
-          // 32 scores of the row, masked. The row is read twice, for its
-          // maximum and for its weights, in loops that stay rolled: unrolled
-          // over a whole row in registers this code outgrew the instruction
-          // cache beside the other roles' and took twice the time (e4m3)
+          // 32 scores of the row, masked. They are read twice, for the maximum
+          // and for the weights, in loops that stay rolled: unrolled over a
+          // whole row in registers this code outgrew the instruction cache
+          // beside the other roles' (a third slower for e4m3)
           auto scores = [&](int c, float (&x)[32]) {
-            tmem_ld32(stm + 32 * c, x);
+            tmem_ld32(stm + kc + 32 * c, x);
             tc_wait_ld();
             if constexpr (E4M3) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float4 s4 = ks[8 * c + e];
+                const float4 s4 = ks[kc / 4 + 8 * c + e];
                 mul2(x[4 * e], x[4 * e + 1], s4.x, s4.y);
                 mul2(x[4 * e + 2], x[4 * e + 3], s4.z, s4.w);
               }
             }
             if (edge) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = (uint32_t)(32 * c + e - first) < (uint32_t)n ? x[e] : kNegInf;
+              for (int e = 0; e < 32; ++e) x[e] = (uint32_t)(kc + 32 * c + e - first) < (uint32_t)n ? x[e] : kNegInf;
             }
           };
           float top = kNegInf;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < (ok ? 2 : 0); ++c) {
             float x[32];
             scores(c, x);
             float t0 = max3f(x[0], x[1], x[2]), t1 = max3f(x[3], x[4], x[5]);
@@ -651,17 +675,21 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
             }
             top = max3f(max3f(t0, x[30], x[31]), t1, top);
           }
-          top *= zs;
+          // the row's maximum over both halves
+          *mx_mine = top;
+          named_bar(pair_bar, 64);
+          top = fmaxf(top, *mx_other) * zs;
           float alpha = 1.f;
           if (top > m + kTau) {
             alpha = fast_exp2(m - top);
             m = top;
           }
           const float off = kGain - (m == kNegInf ? 0.f : m);
-          // P over S, 16 columns behind every 32 read: S(j) landing implies PV(j-1) is complete
+          // P over this half's own columns of S, 16 behind every 32 read: S(j)
+          // landing implies PV(j-1) is complete
           float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < (ok ? 2 : 0); ++c) {
             float x[32];
             scores(c, x);
             uint32_t pk[16];
@@ -674,31 +702,30 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
               add2(sum0, sum1, a, b);
               pk[e] = E4M3 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
             }
-            tmem_st16(stm + 16 * c, pk);
+            tmem_st16(stm + kc + 16 * c, pk);
           }
           l = l * alpha + (sum0 + sum1);
           if constexpr (E4M3) {
-            ok = wait(&sig_full[kk % C::R], kk / C::R);
-            if (!ok) break;
+            ok = ok && wait(&sig_full[kk % C::R], kk / C::R);
             const float now = *reinterpret_cast<const float*>(smem + C::SIG_OFF + (kk % C::R) * 4);
             if (jp > 0) alpha *= sig / now;  // both powers of two
             sig = now;
           }
-          if (jp > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          if (ok && jp > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
+            for (int c = 0; c < D / 32; ++c) {
               float o[16];
-              tmem_ld16(otm + c * 16, o);
+              tmem_ld16(otm + oc + c * 16, o);
               tc_wait_ld();
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] *= alpha;
-              tmem_st16(otm + c * 16, reinterpret_cast<uint32_t*>(o));
+              tmem_st16(otm + oc + c * 16, reinterpret_cast<uint32_t*>(o));
             }
           }
           tc_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(&p_full[w]);
+        if (ok) mbar_arrive(&p_full[w]);
         ++j;
         ++jp;
       }
@@ -713,50 +740,55 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
       const bool whole = q.whole();
       const size_t slot = 2 * (size_t)blockIdx.x + (q.t == 0 ? 1 : 0);
       const size_t obase = ((size_t)(q.b * p.Hkv + q.hk) * p.G * p.N + R) * D;
-      // 32 channels of a row, scaled and stored: the output, or a partial result
-      auto store = [&](int c, float (&o)[32], float f) {
+      // the row's sum over both halves
+      *mx_mine = l;
+      named_bar(pair_bar, 64);
+      l += *mx_other;
+      named_bar(pair_bar, 64);
+      // 16 channels of a row, scaled and stored: the output, or a partial result
+      auto store = [&](int c, float (&o)[16], float f) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] *= f;
+        for (int e = 0; e < 16; ++e) o[e] *= f;
         if (!written) return;
         if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(p.O + obase + c * 32);
+          uint4* dst = reinterpret_cast<uint4*>(p.O + obase + oc + c * 16);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
+          for (int e = 0; e < 2; ++e)
             dst[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
                                 pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
         } else {
           // [slot][four channels][row]: a warp's rows side by side
-          float4* dst = reinterpret_cast<float4*>(wk.o) + (slot * (D / 4) + c * 8) * ROWS + slot_row;
+          float4* dst = reinterpret_cast<float4*>(wk.o) + (slot * (D / 4) + oc / 4 + c * 4) * ROWS + slot_row;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e * ROWS] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          for (int e = 0; e < 4; ++e) dst[e * ROWS] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       };
-      auto load = [&](int c, float (&o)[32]) {
+      auto load = [&](int c, float (&o)[16]) {
         if (have) {
-          tmem_ld32(otm + c * 32, o);
+          tmem_ld16(otm + oc + c * 16, o);
           tc_wait_ld();
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          for (int e = 0; e < 16; ++e) o[e] = 0.f;
         }
       };
       const float unit = E4M3 ? sig * (1.f / 128.f) : 1.f;  // what O is held over
       auto inverse = [&](float x) { return !whole ? 1.f : x > 0.f ? 1.f / x : x == 0.f ? 0.f : x; };
       if constexpr (SPLIT) {
-        // warpgroup 1 hands its half over, 32 channels at a time
-        float4* xch = reinterpret_cast<float4*>(smem + C::XCH_OFF);
+        // row tile 1 hands its results over, 16 channels a warpgroup at a time
+        float4* xch = reinterpret_cast<float4*>(smem + C::XCH_OFF) + hf * 4 * 128;
         float f0 = 0.f, f1 = 0.f;
-        if (w == 1) ml_sh[r] = make_float4(m, l, unit, 0.f);
+        if (w == 1 && hf == 0) ml_sh[r] = make_float4(m, l, unit, 0.f);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
-          float o[32];
+          float o[16];
           load(c, o);
           if (w == 1) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < 4; ++e)
               xch[e * 128 + r] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
-          named_bar(3, 256);
+          named_bar(3, 512);
           if (w == 0) {
             if (c == 0) {
               const float4 x = ml_sh[r];
@@ -768,7 +800,7 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
               f1 = e1 * x.z * inverse(l);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 4; ++e) {
               const float4 x = xch[e * 128 + r];
               o[4 * e] = o[4 * e] * f0 + x.x * f1;
               o[4 * e + 1] = o[4 * e + 1] * f0 + x.y * f1;
@@ -777,18 +809,18 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
             }
             store(c, o, 1.f);
           }
-          named_bar(3, 256);
+          named_bar(3, 512);
         }
       } else {
         const float f = unit * inverse(l);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
-          float o[32];
+          float o[16];
           load(c, o);
           store(c, o, f);
         }
       }
-      if (!whole && written && (!SPLIT || w == 0)) wk.ml[slot * ROWS + slot_row] = make_float2(m, l);
+      if (!whole && written && hf == 0 && (!SPLIT || w == 0)) wk.ml[slot * ROWS + slot_row] = make_float2(m, l);
       if (need.any(w)) {
         tc_fence_before();
         mbar_arrive(&o_free[w]);
@@ -799,7 +831,7 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
   } else {
     if constexpr (E4M3) {
       // ------------------------------------------------------------- converters
-      const int cw = warp - 12;
+      const int cw = warp - 20;
       int c = 0, k = 0;
       bool ok = true;
       while (run.left > 0 && ok) {
