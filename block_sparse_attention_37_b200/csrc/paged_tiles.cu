@@ -149,11 +149,22 @@ struct TileNeed {
     if constexpr (SPLIT) return kt < e0 ? 1 << ((kt - first) & 1) : 0;
     return (kt >= a0 && kt < e0 ? 1 : 0) | (kt >= a1 && kt < e1 ? 2 : 0);
   }
+  // is kt, needed by w, the last that w needs?
+  __device__ __forceinline__ bool last(int kt, int w) const {
+    if constexpr (SPLIT) return kt + 2 >= e0;
+    return kt + 1 == (w ? e1 : e0);
+  }
   __device__ __forceinline__ bool any(int w) const {
     if constexpr (SPLIT) return e0 - first > w;
     return w ? e1 > a1 : e0 > a0;
   }
 };
+
+// The rest of a bounded wait whose first try did not find the phase complete;
+// kept out of line, since the roles' loops share the instruction cache.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
+  return warp_all(mbar_wait(bar, parity, abort_flag, limit_ns));
+}
 
 __device__ __forceinline__ void mul2(float& x0, float& x1, float c0, float c1) {
   uint64_t v, c;
@@ -204,11 +215,11 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
   if (tid == 0) {
     for (int w = 0; w < 2; ++w) {
       mbar_init(&q_full[w], 1);
-      mbar_init(&q_ready[w], 256);
+      mbar_init(&q_ready[w], 8);  // one arrival a warp: 256 on one barrier queue for longer than the softmax
       mbar_init(&s_full[w], 1);
-      mbar_init(&p_full[w], 256);
+      mbar_init(&p_full[w], 8);
       mbar_init(&o_ready[w], 1);
-      mbar_init(&o_free[w], 256);
+      mbar_init(&o_free[w], 8);
     }
     mbar_init(q_empty, 1);
     mbar_init(v_land, 1);
@@ -253,7 +264,8 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
     }
   };
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return warp_all(mbar_wait(bar, parity & 1u, abort_flag, p.wait_limit_ns));
+    const uint32_t a = smem_u32(bar);
+    return warp_all(mbar_try_wait(a, parity & 1u)) || wait_slow(bar, parity & 1u, abort_flag, p.wait_limit_ns);
   };
   const int page_mask = (1 << p.page_log2) - 1;
 
@@ -438,89 +450,104 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
       constexpr uint32_t idesc_qk = E4M3 ? idesc_e4m3_f32(128, 128) : idesc_bf16_f32(128, 128, false, false);
       constexpr uint32_t idesc_pv = E4M3 ? idesc_f16_f32(128, D, true) : idesc_bf16_f32(128, D, false, true);
       const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV);
-      int pt0 = -1, pt1 = -1;    // tile whose PV is outstanding, per row tile
-      int np0 = 0, np1 = 0;      // PVs issued
-      int nf0 = 0, nf1 = 0;      // pieces begun
-      bool new0 = false, new1 = false;  // the next PV is the piece's first
+      struct RowTile {
+        int pt;      // tile whose PV is outstanding (-1: none)
+        int np, nf;  // PVs issued, pieces begun
+        bool fresh;  // the next PV is the piece's first
+        bool last;   // the outstanding PV is the piece's last
+      };
+      RowTile cur{-1, 0, 0, false, false}, oth = cur;
       int v_seen = 0, k = 0, pc = 0;
-      uint32_t rem = 0u;         // row tiles still to use a stage's V, two bits a stage
+      uint32_t rem = 0u;  // row tiles still to use a stage's V, two bits a stage
       bool ok = true, issued = false;
-      // V tiles are observed in tile order, so the parity test never meets
-      // another phase of a shared stage
-      auto pv = [&](int w) -> bool {
-        const int u = w ? pt1 : pt0, st = u % SV;
-        for (; v_seen <= u; ++v_seen)
-          if (!wait(&v_full[v_seen % SV], v_seen / SV)) return false;
-        bool& fresh = w ? new1 : new0;
-        if (fresh) {  // O of the piece before has been read
-          int& nf = w ? nf1 : nf0;
-          if (nf > 0 && !wait(&o_free[w], nf - 1)) return false;
-          ++nf;
-        }
-        int& np = w ? np1 : np0;
-        if (!wait(&p_full[w], np)) return false;
-        ++np;
-        tc_fence_after();
-        pv_halves(tmem + 256 + w * D, tmem + 128 * w, smem_desc_sw128(sVa + st * C::VTILE, C::CHUNK, 1024), idesc_pv,
-                  fresh ? 1u : 0u, std::make_integer_sequence<int, 8>{});
-        fresh = false;
-        tc_commit_warp(&o_ready[w]);
-        rem -= 1u << (2 * st);
-        if (((rem >> (2 * st)) & 3u) == 0u) tc_commit_warp(&v_empty[st]);
-        (w ? pt1 : pt0) = -1;
-        return true;
-      };
-      // outstanding PVs of tiles below `limit`, oldest first
-      auto flush_below = [&](int limit) -> bool {
-        const bool f0 = pt0 >= 0 && pt0 < limit, f1 = pt1 >= 0 && pt1 < limit;
-        if (f0 && f1 && pt1 < pt0) return pv(1) && pv(0);
-        return (!f0 || pv(0)) && (!f1 || pv(1));
-      };
-      auto qk = [&](int w, int st) {
-        tc_fence_after();
-        const uint32_t qa = sQa + (SPLIT ? 0 : w) * C::QTILE, ka = sKa + st * C::KTILE;
-        if constexpr (!E4M3) {
-          qk_all(tmem + 128 * w, smem_desc_sw128(qa, 16, 1024), smem_desc_sw128(ka, 16, 1024), idesc_qk,
-                 std::make_integer_sequence<int, D / 16>{});
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)  // the row's rounding, then the rest
-            qk8_sum(tmem + 128 * w,
-                    D == 128 ? smem_desc_sw128(qa + h * 128 * D, 16, 1024) : smem_desc_sw64(qa + h * 128 * D),
-                    D == 128 ? smem_desc_sw128(ka, 16, 1024) : smem_desc_sw64(ka), idesc_qk, (uint32_t)h,
-                    std::make_integer_sequence<int, D / 32>{});
-        }
-        tc_commit_warp(&s_full[w]);
-        issued = true;
-      };
+      // One code site for PV and one for QK^T, the row tiles taking turns in
+      // `cur`: with a copy a call this loop alone outgrew the instruction cache.
       for (; run.left > 0 && ok; ++pc) {
         const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
         const TileNeed<SPLIT> need(p, q);
         for (int w = 0; w < (SPLIT ? 1 : 2) && ok; ++w) ok = wait(E4M3 ? &q_ready[w] : &q_full[w], pc);
-        new0 = new1 = true;
-        for (int i = 0; i < q.m && ok; ++i) {
-          const int nw = need.mask(q.s.t0 + q.t + i);
-          if (nw == 0) continue;
+        cur.fresh = oth.fresh = true;
+#pragma unroll 1
+        for (int i = 0; i <= q.m && ok; ++i) {
+          const int kt = q.s.t0 + q.t + i;
+          const bool flush = i == q.m;  // the piece's last PVs
+          const int nw = flush ? 0 : need.mask(kt);
+          if (nw == 0 && !flush) continue;
           const int st = k % SK;
-          ok = wait(&k_full[st], k / SK) && flush_below(k - SV + 1);
-          if (!ok) break;
-          rem |= (uint32_t)__popc(nw) << (2 * (k % SV));
-          if (nw & 1) {
-            if (pt0 >= 0 && !(ok = pv(0))) break;
-            qk(0, st);
-            pt0 = k;
+          if (!flush)
+            ok = wait(&k_full[st], k / SK);
+          else
+            tc_commit_warp(q_empty);
+          // a row tile that does not need tile k goes first: its outstanding
+          // PV may be the last user of the V stage tile k is about to count on
+          const int w0 = nw == 1 ? 1 : 0;
+          if (w0) {
+            const RowTile t = cur;
+            cur = oth;
+            oth = t;
           }
-          if (nw & 2) {
-            if (pt1 >= 0 && !(ok = pv(1))) break;
-            qk(1, st);
-            pt1 = k;
+#pragma unroll 1
+          for (int s = 0; s < 2; ++s) {
+            const int w = w0 ^ s;
+            // PV of the tile before: P lies over S, and the tensor pipe keeps
+            // issue order. One that holds up the V stage of tile k goes out
+            // although its row tile does not need tile k.
+            if (ok && cur.pt >= 0 && (flush || ((nw >> w) & 1) || cur.pt <= k - SV)) {
+              const int u = cur.pt, sv = u % SV;
+              // V tiles are observed in tile order, so the parity test never
+              // meets another phase of a shared stage
+              for (; v_seen <= u && ok; ++v_seen) ok = wait(&v_full[v_seen % SV], v_seen / SV);
+              if (cur.fresh) {  // O of the piece before has been read
+                if (cur.nf > 0) ok = ok && wait(&o_free[w], cur.nf - 1);
+                ++cur.nf;
+              }
+              ok = ok && wait(&p_full[w], cur.np);
+              ++cur.np;
+              if (ok) {
+                tc_fence_after();
+                pv_halves(tmem + 256 + w * D, tmem + 128 * w, smem_desc_sw128(sVa + sv * C::VTILE, C::CHUNK, 1024),
+                          idesc_pv, cur.fresh ? 1u : 0u, std::make_integer_sequence<int, 8>{});
+                if (cur.last) tc_commit_warp(&o_ready[w]);
+                rem -= 1u << (2 * sv);
+                if (((rem >> (2 * sv)) & 3u) == 0u) tc_commit_warp(&v_empty[sv]);
+              }
+              cur.fresh = false;
+              cur.pt = -1;
+            }
+            if (ok && ((nw >> w) & 1)) {
+              tc_fence_after();
+              const uint32_t qa = sQa + (SPLIT ? 0 : w) * C::QTILE, ka = sKa + st * C::KTILE;
+              if constexpr (!E4M3) {
+                qk_all(tmem + 128 * w, smem_desc_sw128(qa, 16, 1024), smem_desc_sw128(ka, 16, 1024), idesc_qk,
+                       std::make_integer_sequence<int, D / 16>{});
+              } else {
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h)  // the row's rounding, then the rest
+                  qk8_sum(tmem + 128 * w,
+                          D == 128 ? smem_desc_sw128(qa + h * 128 * D, 16, 1024) : smem_desc_sw64(qa + h * 128 * D),
+                          D == 128 ? smem_desc_sw128(ka, 16, 1024) : smem_desc_sw64(ka), idesc_qk, (uint32_t)h,
+                          std::make_integer_sequence<int, D / 32>{});
+              }
+              tc_commit_warp(&s_full[w]);
+              issued = true;
+              rem += 1u << (2 * (k % SV));
+              cur.pt = k;
+              cur.last = need.last(kt, w);
+            }
+            const RowTile t = cur;
+            cur = oth;
+            oth = t;
           }
-          tc_commit_warp(&k_empty[st]);
-          ++k;
+          if (w0) {
+            const RowTile t = cur;
+            cur = oth;
+            oth = t;
+          }
+          if (!flush) {
+            tc_commit_warp(&k_empty[st]);
+            ++k;
+          }
         }
-        if (!ok) break;
-        tc_commit_warp(q_empty);
-        ok = flush_below(k);
       }
       if (!ok) cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
       // tensor memory is freed only once every issued MMA has completed
@@ -543,7 +570,7 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
     const int slot_row = (SPLIT ? 0 : 128 * w) + r;  // row of the item
     float4* ml_sh = reinterpret_cast<float4*>(smem + C::ML_OFF);
     float* zs_sh = reinterpret_cast<float*>(smem + C::ZS_OFF);
-    int j = 0, k = 0, pc = 0;  // tiles of this row tile, tiles and pieces of the CTA
+    int j = 0, pj = 0, k = 0, pc = 0;  // tiles and pieces of this row tile, tiles and pieces of the CTA
     bool ok = true;
     SplitItem split{0, 0, 0, 0};
     for (; run.left > 0; ++pc) {
@@ -616,7 +643,8 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
             if (hf == 0) zs_sh[r] = zs;
           if (!ok) cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
           fence_proxy_async_smem();
-          mbar_arrive(&q_ready[w]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_ready[w]);
         } else {
           // row tile 0's warpgroups convert; they cannot pass this piece's join
           // before this one
@@ -725,12 +753,13 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
           tc_wait_st();
         }
         tc_fence_before();
-        if (ok) mbar_arrive(&p_full[w]);
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&p_full[w]);
         ++j;
         ++jp;
       }
-      if (ok && jp > 0) {
-        ok = wait(&o_ready[w], j - 1);
+      if (jp > 0) {
+        ok = ok && wait(&o_ready[w], pj++);
         tc_fence_after();
       }
       if (!ok) cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
@@ -823,7 +852,8 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
       if (!whole && written && hf == 0 && (!SPLIT || w == 0)) wk.ml[slot * ROWS + slot_row] = make_float2(m, l);
       if (need.any(w)) {
         tc_fence_before();
-        mbar_arrive(&o_free[w]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[w]);
       }
     }
     if (warp == 4 && lane == 0) wk.split[blockIdx.x] = split;
