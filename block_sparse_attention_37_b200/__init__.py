@@ -384,7 +384,7 @@ class PagedCache:
     [n_pages, Hkv, page]; table is int32 [B, max_pages], kv_len int32 [B]. The tensors are the
     caller's: their contents may change between calls (pages filled, kv_len raised), the tensors
     of a PagedCache may not."""
-    __slots__ = ("k", "v", "table", "kv_len", "k_scale", "v_scale", "device", "_c", "_ref")
+    __slots__ = ("k", "v", "table", "kv_len", "k_scale", "v_scale", "device", "_c", "_ref", "_index", "_B", "_Hkv")
 
     def __init__(self, k, v, table, kv_len, k_scale=None, v_scale=None):
         e4m3 = isinstance(k, torch.Tensor) and k.dtype == torch.uint8
@@ -418,7 +418,7 @@ class PagedCache:
         self.k, self.v, self.table, self.kv_len = k, v, table, kv_len
         self.k_scale, self.v_scale, self.device = k_scale, v_scale, k.device
         self._c = PagedCacheC(CACHE_E4M3 if e4m3 else CACHE_BF16, n_pages, Hkv, page, d, table.shape[1], *p)
-        self._ref = ctypes.byref(self._c)
+        self._ref, self._index, self._B, self._Hkv = ctypes.byref(self._c), k.get_device(), table.shape[0], Hkv
 
     @classmethod
     def empty(cls, n_pages, Hkv, page, d, B, max_pages, kind=CACHE_BF16, device="cuda") -> "PagedCache":
@@ -433,18 +433,18 @@ class PagedCache:
                    torch.zeros((B,), dtype=torch.int32, device=device), sc(), sc())
 
     def _chunk(self, dm: Dims) -> int:
-        """Elements of this call's [B, Hkv, N, d] chunk; refuses dims that are not the cache's."""
-        if dm.B != self.kv_len.shape[0]:
-            raise ValueError(f"dims hold {dm.B} sequences, the cache's table {self.kv_len.shape[0]}")
-        return dm.B * self._c.Hkv * max(dm.N, 0) * max(dm.d, 0)
+        """Elements of one head of this call's chunk, B * N * d; refuses dims that are not the cache's."""
+        B = dm.B
+        if B != self._B:
+            raise ValueError(f"dims hold {B} sequences, the cache's table {self._B}")
+        return B * max(dm.N, 0) * max(dm.d, 0)
 
 
 def _paged_ptr(cache: PagedCache, t, dtype, name, numel):
-    """_ptr for the calls on a cache, whose launches are short enough for the checks to show:
-    one test of everything, and _ptr to say what is wrong. The tensor must be on the cache's
-    device, which is made current for the call (see _on)."""
-    if (type(t) is torch.Tensor and t.dtype is dtype and t.numel() >= numel and t.is_contiguous()
-            and t.device == cache.device and t.is_cuda):
+    """_ptr for the calls on a cache, whose launches are short enough for the checks to show: one
+    test of everything, and _ptr to say what is wrong. The tensor must be on the cache's device."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == cache._index >= 0
+            and t.numel() >= numel and t.is_contiguous()):
         return t.data_ptr()
     if t is None:
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -454,33 +454,36 @@ def _paged_ptr(cache: PagedCache, t, dtype, name, numel):
     return p
 
 
-def _on(cache: PagedCache, where: str, call, stream):
-    """call(stream) with the cache's device current, on `stream` or that device's current stream."""
-    if cache.device.type == "cuda" and cache.device.index != torch.cuda.current_device():
-        with torch.cuda.device(cache.device):
-            return _check(call(_stream(stream)), where)
-    return _check(call(_stream(stream)), where)
+def _paged_call(cache: PagedCache, name: str, stream, *args):
+    """The library call `name` with the cache's device current, on `stream` or that device's
+    current stream (asked for by its raw handle: a torch Stream object costs as much as a launch)."""
+    i = cache._index
+    if i >= 0 and i != torch._C._cuda_getDevice():
+        with torch.cuda.device(i):
+            return _paged_call(cache, name, stream, *args)
+    raw = torch._C._cuda_getCurrentRawStream(i) if stream is None and i >= 0 else _stream(stream)
+    status = getattr(_lib(), name)(*args, raw)
+    if status != OK:
+        raise BsaError(status, name)
 
 
 def paged_append(dm: Dims, cache: PagedCache, k, v, n_new=None, stream=None):
     """bsa_paged_append: write a chunk's k and v (cuda bf16 [B, Hkv, N, d]) at the end of each
     sequence, positions kv_len - n_new .. kv_len - 1 (set kv_len to the new lengths first).
     n_new: cuda int32 [B], the chunk's tokens per sequence, or None (N each)."""
-    n = cache._chunk(dm)
-    kp, vp = _paged_ptr(cache, k, torch.bfloat16, "K", n), _paged_ptr(cache, v, torch.bfloat16, "V", n)
-    np_ = _paged_ptr(cache, n_new, torch.int32, "n_new", dm.B) if n_new is not None else None
-    lib = _lib()
-    _on(cache, "bsa_paged_append", lambda s: lib.bsa_paged_append(ctypes.byref(dm), kp, vp, np_, cache._ref, s), stream)
+    n = cache._chunk(dm) * cache._Hkv
+    _paged_call(cache, "bsa_paged_append", stream, ctypes.byref(dm),
+                _paged_ptr(cache, k, torch.bfloat16, "K", n), _paged_ptr(cache, v, torch.bfloat16, "V", n),
+                _paged_ptr(cache, n_new, torch.int32, "n_new", cache._B) if n_new is not None else None, cache._ref)
 
 
 def paged_read(dm: Dims, cache: PagedCache, k, v, begin=None, stream=None):
     """bsa_paged_read: tokens begin .. begin + N - 1 of each sequence into k and v (cuda bf16
     [B, Hkv, N, d]), zeros past its end. begin: cuda int32 [B], or None (0)."""
-    n = cache._chunk(dm)
-    kp, vp = _paged_ptr(cache, k, torch.bfloat16, "K", n), _paged_ptr(cache, v, torch.bfloat16, "V", n)
-    bp = _paged_ptr(cache, begin, torch.int32, "begin", dm.B) if begin is not None else None
-    lib = _lib()
-    _on(cache, "bsa_paged_read", lambda s: lib.bsa_paged_read(ctypes.byref(dm), cache._ref, bp, kp, vp, s), stream)
+    n = cache._chunk(dm) * cache._Hkv
+    _paged_call(cache, "bsa_paged_read", stream, ctypes.byref(dm), cache._ref,
+                _paged_ptr(cache, begin, torch.int32, "begin", cache._B) if begin is not None else None,
+                _paged_ptr(cache, k, torch.bfloat16, "K", n), _paged_ptr(cache, v, torch.bfloat16, "V", n))
 
 
 def paged_workspace_size(dm: Dims, cache: PagedCache) -> int:
@@ -497,16 +500,12 @@ def paged_forward(dm: Dims, cache: PagedCache, q, o, workspace, n_new=None, caus
     the last `window` of them; otherwise every cached token. workspace: cuda tensor of at least
     paged_workspace_size bytes, 256-byte aligned, not shared with a call that may overlap; scale
     defaults to 1/sqrt(d)."""
-    scale = (1.0 / dm.d ** 0.5) if scale is None else scale
-    cache._chunk(dm)
-    n = _tokens(dm)
-    qp, op = _paged_ptr(cache, q, torch.bfloat16, "Q", n), _paged_ptr(cache, o, torch.bfloat16, "O", n)
-    np_ = _paged_ptr(cache, n_new, torch.int32, "n_new", dm.B) if n_new is not None else None
+    n = cache._chunk(dm) * max(dm.H, 0)
     wp = _paged_ptr(cache, workspace, getattr(workspace, "dtype", None), "workspace", 0)
-    wb = workspace.numel() * workspace.element_size()
-    lib = _lib()
-    _on(cache, "bsa_paged_forward", lambda s: lib.bsa_paged_forward(
-        ctypes.byref(dm), qp, np_, cache._ref, 1 if causal else 0, window, float(scale), wp, wb, op, s), stream)
+    _paged_call(cache, "bsa_paged_forward", stream, ctypes.byref(dm), _paged_ptr(cache, q, torch.bfloat16, "Q", n),
+                _paged_ptr(cache, n_new, torch.int32, "n_new", cache._B) if n_new is not None else None, cache._ref,
+                1 if causal else 0, window, 1.0 / dm.d ** 0.5 if scale is None else float(scale), wp,
+                workspace.numel() * workspace.element_size(), _paged_ptr(cache, o, torch.bfloat16, "O", n))
 
 
 def gna_tiled_len(n_text: int, gna: GnaGeom) -> int:
