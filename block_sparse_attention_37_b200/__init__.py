@@ -487,7 +487,11 @@ def paged_read(dm: Dims, cache: PagedCache, k, v, begin=None, stream=None):
 
 
 def paged_workspace_size(dm: Dims, cache: PagedCache) -> int:
-    """Bytes of device workspace paged_forward needs for these dims and cache, whatever the lengths."""
+    """Bytes of device workspace paged_forward needs for these dims and cache on the cache's device,
+    whatever the lengths."""
+    if getattr(cache, "_index", -1) >= 0 and cache._index != torch._C._cuda_getDevice():
+        with torch.cuda.device(cache._index):
+            return paged_workspace_size(dm, cache)
     return int(_lib().bsa_paged_workspace_size(ctypes.byref(dm), cache._ref))
 
 

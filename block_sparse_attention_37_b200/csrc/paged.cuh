@@ -25,6 +25,7 @@ struct PagedParams {
   __nv_bfloat16* O;
   int G;                   // query heads a key/value head
   int causal, window;
+  int whole_items;         // runs hold whole items: nothing is split
   float scale_log2;        // scale * log2(e)
   uint64_t wait_limit_ns;  // failure detection: as in AttnParams
   int withhold_tile;

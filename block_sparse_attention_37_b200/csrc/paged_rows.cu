@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
   const int cta = blockIdx.x;
 
   asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before may have written what is read here
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
@@ -596,6 +597,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, co
   constexpr int V = D / 32;
   __shared__ float acc_sh[8][D];
   __shared__ float l_sh[8];
+  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const SplitItem it = wk.split[blockIdx.x];
   if (it.parts <= 1) return;
@@ -643,11 +645,14 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, co
   }
 }
 
+// A launch that may be scheduled while the kernel before it finishes; every
+// kernel launched so waits (griddepcontrol.wait) before it reads memory.
 template <class K, class... A>
-static cudaError_t launch_after(K kernel, dim3 grid, unsigned block, cudaStream_t stream, A... args) {
+static cudaError_t launch_after(K kernel, dim3 grid, unsigned block, size_t smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -666,10 +671,10 @@ static cudaError_t launch_rows_d(const CUtensorMap& k, const CUtensorMap& v, con
   cudaError_t e = once.run(
       [&]() -> cudaError_t { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC); });
   if (e != cudaSuccess) return e;
-  fn<<<grid, C::THREADS, C::ALLOC, stream>>>(k, v, p, w);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_after(fn, dim3(grid), C::THREADS, C::ALLOC, stream, k, v, p, w)) != cudaSuccess) return e;
+  if (p.whole_items) return cudaSuccess;
   const int rows = p.G * p.N;
-  return launch_after(paged_join_kernel<D, kRowsTile>, dim3(grid, min(rows, 8)), 256, stream, p, w, 1);
+  return launch_after(paged_join_kernel<D, kRowsTile>, dim3(grid, min(rows, 8)), 256, 0, stream, p, w, 1);
 }
 
 template <int D, bool E4M3>

@@ -14,6 +14,8 @@
 // one for the item it ends in. The item's first CTA names it to the combine
 // kernel, which joins the partials in the order of the CTAs: the result does
 // not depend on timing.
+// Where the table's width bounds every item to a few tiles, the line counts
+// items instead (whole_items): nothing is split and no join is launched.
 #pragma once
 
 #include "paged.cuh"
@@ -109,6 +111,11 @@ struct PagedWork {
 // scratch of 2 + NT / 32 long longs plus a Run behind a barrier). Each thread
 // sums a chunk of the items, a scan places the chunks on the line, and the
 // thread whose chunk holds the run's start looks it up.
+// An item's length on the line.
+__device__ __forceinline__ int line_tiles(const PagedParams& p, const ItemSpan& s) {
+  return p.whole_items ? (s.nt > 0) : s.nt;
+}
+
 template <int ROWS, int KT, int NT>
 __device__ Run find_run(const PagedParams& p, int row_tiles, int min_tiles, Run* run_sh, long long* sh) {
   constexpr int W = NT / 32;
@@ -122,7 +129,7 @@ __device__ Run find_run(const PagedParams& p, int row_tiles, int min_tiles, Run*
     SeqLen s;
     if (i / row_tiles != b) b = i / row_tiles;
     s = seq_lens(p, b);
-    sum += item_span<ROWS, KT>(p, s.n, s.kv, i - b * row_tiles).nt;
+    sum += line_tiles(p, item_span<ROWS, KT>(p, s.n, s.kv, i - b * row_tiles));
   }
   long long inc = sum;
 #pragma unroll
@@ -139,7 +146,7 @@ __device__ Run find_run(const PagedParams& p, int row_tiles, int min_tiles, Run*
     all += sh[w];
   }
   const long long total = all * p.Hkv;
-  const int ctas = run_ctas(total, gridDim.x, min_tiles);
+  const int ctas = run_ctas(total, gridDim.x, p.whole_items ? 1 : min_tiles);
   const int c = blockIdx.x;
   const long long s0 = c < ctas ? run_start(total, c, ctas) : total;
   const long long s1 = c < ctas ? run_start(total, c + 1, ctas) : total;
@@ -149,7 +156,7 @@ __device__ Run find_run(const PagedParams& p, int row_tiles, int min_tiles, Run*
     for (int i = first; i < last; ++i) {
       const int b = i / row_tiles;
       const SeqLen s = seq_lens(p, b);
-      const int nt = item_span<ROWS, KT>(p, s.n, s.kv, i - b * row_tiles).nt;
+      const int nt = line_tiles(p, item_span<ROWS, KT>(p, s.n, s.kv, i - b * row_tiles));
       const long long w = (long long)nt * p.Hkv;
       if (s0 < at + w) {
         const long long d = s0 - at;
@@ -188,9 +195,10 @@ __device__ __forceinline__ Piece next_piece(const PagedParams& p, int row_tiles,
   q.hk = r.hk;
   q.t = r.t;
   const long long rest = q.s.nt - q.t;
-  q.m = (int)(rest < r.left ? rest : r.left);
-  r.left -= q.m;
-  r.pos += q.m;
+  q.m = p.whole_items || rest < r.left ? (int)rest : (int)r.left;
+  const int step = p.whole_items ? 1 : q.m;
+  r.left -= step;
+  r.pos += step;
   r.t = 0;
   if (++r.hk == p.Hkv) {
     r.hk = 0;

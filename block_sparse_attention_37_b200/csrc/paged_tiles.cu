@@ -160,8 +160,15 @@ struct TileNeed {
   }
 };
 
+// 32 lanes x 32-bit, 8 consecutive columns per thread.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // The rest of a bounded wait whose first try did not find the phase complete;
-// kept out of line, since the roles' loops share the instruction cache.
+// kept out of line for e4m3, whose roles' loops outgrow the instruction cache.
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
   return warp_all(mbar_wait(bar, parity, abort_flag, limit_ns));
 }
@@ -265,7 +272,9 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
   };
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     const uint32_t a = smem_u32(bar);
-    return warp_all(mbar_try_wait(a, parity & 1u)) || wait_slow(bar, parity & 1u, abort_flag, p.wait_limit_ns);
+    if (warp_all(mbar_try_wait(a, parity & 1u))) return true;
+    if constexpr (E4M3) return wait_slow(bar, parity & 1u, abort_flag, p.wait_limit_ns);
+    return warp_all(mbar_wait(bar, parity & 1u, abort_flag, p.wait_limit_ns));
   };
   const int page_mask = (1 << p.page_log2) - 1;
 
@@ -460,8 +469,9 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
       int v_seen = 0, k = 0, pc = 0;
       uint32_t rem = 0u;  // row tiles still to use a stage's V, two bits a stage
       bool ok = true, issued = false;
-      // One code site for PV and one for QK^T, the row tiles taking turns in
-      // `cur`: with a copy a call this loop alone outgrew the instruction cache.
+      // e4m3: one code site for PV and one for QK^T, the row tiles taking turns
+      // in `cur`; with a copy a call this loop outgrew the instruction cache
+      // (ragged chunks 342 -> 275 us). bf16 has room for a copy a row tile.
       for (; run.left > 0 && ok; ++pc) {
         const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
         const TileNeed<SPLIT> need(p, q);
@@ -486,7 +496,7 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
             cur = oth;
             oth = t;
           }
-#pragma unroll 1
+#pragma unroll(E4M3 ? 1 : 2)
           for (int s = 0; s < 2; ++s) {
             const int w = w0 ^ s;
             // PV of the tile before: P lies over S, and the tensor pipe keeps
@@ -670,38 +680,44 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
           if constexpr (E4M3) ok = ok && wait(&sc_full[kk % C::R], kk / C::R);
           const bool edge = key0 < clo || key0 + kTileKeys > chi;
           const int first = lo - key0, n = hi - lo;  // the row keeps columns [first, first + n)
-          // 32 scores of the row, masked. They are read twice, for the maximum
+          // CH scores of the row, masked. They are read twice, for the maximum
           // and for the weights, in loops that stay rolled: unrolled over a
           // whole row in registers this code outgrew the instruction cache
-          // beside the other roles' (a third slower for e4m3)
-          auto scores = [&](int c, float (&x)[32]) {
-            tmem_ld32(stm + kc + 32 * c, x);
+          // beside the other roles' (a third slower for e4m3). The converters'
+          // threads leave e4m3 fewer registers (16 scores at a time: 264 us
+          // for the ragged chunks, 32: 274).
+          constexpr int CH = E4M3 ? 16 : 32;
+          auto scores = [&](int c, float (&x)[CH]) {
+            if constexpr (CH == 32)
+              tmem_ld32(stm + kc + CH * c, x);
+            else
+              tmem_ld16(stm + kc + CH * c, x);
             tc_wait_ld();
             if constexpr (E4M3) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 s4 = ks[kc / 4 + 8 * c + e];
+              for (int e = 0; e < CH / 4; ++e) {
+                const float4 s4 = ks[kc / 4 + CH / 4 * c + e];
                 mul2(x[4 * e], x[4 * e + 1], s4.x, s4.y);
                 mul2(x[4 * e + 2], x[4 * e + 3], s4.z, s4.w);
               }
             }
             if (edge) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = (uint32_t)(kc + 32 * c + e - first) < (uint32_t)n ? x[e] : kNegInf;
+              for (int e = 0; e < CH; ++e) x[e] = (uint32_t)(kc + CH * c + e - first) < (uint32_t)n ? x[e] : kNegInf;
             }
           };
           float top = kNegInf;
 #pragma unroll 1
-          for (int c = 0; c < (ok ? 2 : 0); ++c) {
-            float x[32];
+          for (int c = 0; c < (ok ? 64 / CH : 0); ++c) {
+            float x[CH];
             scores(c, x);
             float t0 = max3f(x[0], x[1], x[2]), t1 = max3f(x[3], x[4], x[5]);
 #pragma unroll
-            for (int e = 6; e < 30; e += 4) {
+            for (int e = 6; e < CH - 2; e += 4) {
               t0 = max3f(t0, x[e], x[e + 1]);
               t1 = max3f(t1, x[e + 2], x[e + 3]);
             }
-            top = max3f(max3f(t0, x[30], x[31]), t1, top);
+            top = max3f(max3f(t0, x[CH - 2], x[CH - 1]), t1, top);
           }
           // the row's maximum over both halves
           *mx_mine = top;
@@ -713,16 +729,16 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
             m = top;
           }
           const float off = kGain - (m == kNegInf ? 0.f : m);
-          // P over this half's own columns of S, 16 behind every 32 read: S(j)
+          // P over this half's own columns of S, behind the scores read: S(j)
           // landing implies PV(j-1) is complete
           float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < (ok ? 2 : 0); ++c) {
-            float x[32];
+          for (int c = 0; c < (ok ? 64 / CH : 0); ++c) {
+            float x[CH];
             scores(c, x);
-            uint32_t pk[16];
+            uint32_t pk[CH / 2];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < CH / 2; ++e) {
               float a = x[2 * e], b = x[2 * e + 1];
               fma2(a, b, zs, off);
               a = fast_exp2(a);
@@ -730,7 +746,10 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
               add2(sum0, sum1, a, b);
               pk[e] = E4M3 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
             }
-            tmem_st16(stm + kc + 16 * c, pk);
+            if constexpr (CH == 32)
+              tmem_st16(stm + kc + 16 * c, pk);
+            else
+              tmem_st8(stm + kc + 8 * c, pk);
           }
           l = l * alpha + (sum0 + sum1);
           if constexpr (E4M3) {
@@ -943,40 +962,51 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
 }
 
 // Joins the partial results of split items (see paged_join_kernel): grid
-// (CTAs of the forward, y), a thread a row and four channels, rows side by
-// side as they were stored.
+// (CTAs of the forward, 8), a thread a row and some groups of four channels,
+// rows side by side as they were stored.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(256) paged_join_tiles_kernel(const PagedParams p, const PagedWork wk, int row_tiles) {
+  constexpr int CPT = ROWS * (D / 4) / 2048;  // channel groups a thread
+  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const SplitItem it = wk.split[blockIdx.x];
   if (it.parts <= 1) return;
   const int b = it.idx / row_tiles, rt = it.idx - b * row_tiles;
   const SeqLen s = clamp_lens(p, p.n_new ? __ldg(p.n_new + b) : p.N, __ldg(p.kv_len + b));
+  const int x = blockIdx.y * 256 + threadIdx.x;
+  const int r = x % ROWS, c0 = x / ROWS;  // channel groups c0, c0 + 2048 / ROWS, ...
+  const int R = rt * ROWS + r;
+  if (R >= p.G * p.N || R - fdiv(R, p.f_n) * p.N >= s.n) return;
   auto slot = [&](int i) -> size_t { return i == 0 ? 2 * (size_t)blockIdx.x + 1 : 2 * ((size_t)blockIdx.x + i); };
-  for (int x = blockIdx.y * 256 + threadIdx.x; x < ROWS * (D / 4); x += gridDim.y * 256) {
-    const int r = x % ROWS, c4 = x / ROWS;
-    const int R = rt * ROWS + r;
-    if (R >= p.G * p.N || R - fdiv(R, p.f_n) * p.N >= s.n) continue;
-    float m = kNegInf, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  // the maximum first: the sums over the parts are then independent loads
+  float m = kNegInf, l = 0.f;
 #pragma unroll 4
-    for (int i = 0; i < it.parts; ++i) {
-      const float2 ml = wk.ml[slot(i) * ROWS + r];
-      const float4 o = reinterpret_cast<const float4*>(wk.o)[(slot(i) * (D / 4) + c4) * ROWS + r];
-      const float M = fmaxf(m, ml.x), mu = M == kNegInf ? 0.f : M;
-      const float e0 = fast_exp2(m - mu), e1 = fast_exp2(ml.x - mu);
-      m = M;
-      l = l * e0 + ml.y * e1;
-      acc.x = acc.x * e0 + o.x * e1;
-      acc.y = acc.y * e0 + o.y * e1;
-      acc.z = acc.z * e0 + o.z * e1;
-      acc.w = acc.w * e0 + o.w * e1;
+  for (int i = 0; i < it.parts; ++i) m = fmaxf(m, wk.ml[slot(i) * ROWS + r].x);
+  const float mu = m == kNegInf ? 0.f : m;
+  float4 acc[CPT];
+#pragma unroll
+  for (int c = 0; c < CPT; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < it.parts; ++i) {
+    const float2 ml = wk.ml[slot(i) * ROWS + r];
+    const float4* o = reinterpret_cast<const float4*>(wk.o) + (slot(i) * (D / 4) + c0) * ROWS + r;
+    const float e = fast_exp2(ml.x - mu);
+    l += ml.y * e;
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) {
+      const float4 v = o[c * 2048];
+      acc[c].x += v.x * e;
+      acc[c].y += v.y * e;
+      acc[c].z += v.z * e;
+      acc[c].w += v.w * e;
     }
-    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-    const size_t at = ((size_t)(b * p.Hkv + it.hk) * p.G * p.N + R) * D + 4 * c4;
-    *reinterpret_cast<uint2*>(p.O + at) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   }
+  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+  __nv_bfloat16* dst = p.O + ((size_t)(b * p.Hkv + it.hk) * p.G * p.N + R) * D + 4 * c0;
+#pragma unroll
+  for (int c = 0; c < CPT; ++c)
+    *reinterpret_cast<uint2*>(dst + c * (4 * 2048 / ROWS)) =
+        make_uint2(pack_bf16x2(acc[c].x * inv, acc[c].y * inv), pack_bf16x2(acc[c].z * inv, acc[c].w * inv));
 }
 
 template <int D, bool E4M3, bool SPLIT>
@@ -990,10 +1020,12 @@ static cudaError_t launch_tiles_d(const CUtensorMap& q, const CUtensorMap& k, co
     return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::ALLOC);
   });
   if (e != cudaSuccess) return e;
+  // (a dependent launch gains nothing here: a CTA takes an SM of its own)
   fn<<<grid, C::THREADS, C::ALLOC, stream>>>(q, k, v, p, w, row_tiles);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (p.whole_items) return cudaSuccess;
   constexpr int ROWS = SPLIT ? 128 : 256;
-  return launch_after(paged_join_tiles_kernel<D, ROWS>, dim3(grid, 8), 256, stream, p, w, row_tiles);
+  return launch_after(paged_join_tiles_kernel<D, ROWS>, dim3(grid, 8), 256, 0, stream, p, w, row_tiles);
 }
 
 template <int D, bool E4M3>

@@ -172,6 +172,10 @@ CASES = [  # H, Hkv, N, page, kv_len, n_new, causal, window
     (2, 2, 300, 64, [300, 1111], [300, 257], True, 130),
     (1, 1, 513, 64, [2000], None, False, 0),
     (5, 1, 107, 16, [900, 107], [107, 50], True, 300),
+    # one head over many tiles: an item split over most of the GPU
+    (2, 1, 1, 64, [20000], None, True, 0),
+    (1, 1, 33, 128, [20001], None, False, 0),
+    (1, 1, 260, 32, [9000], None, True, 0),
 ]
 
 
@@ -180,6 +184,101 @@ CASES = [  # H, Hkv, N, page, kv_len, n_new, causal, window
 @pytest.mark.parametrize("kind", [BF16, E4M3])
 def test_forward_matches_the_oracle(kind, d, H, Hkv, N, page, kv, n_new, causal, window):
     _check(kind, H, Hkv, N, d, page, kv, n_new, causal, window)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("kind", [BF16, E4M3])
+@pytest.mark.parametrize("H,N", [(2, 1), (2, 20), (2, 150)])
+def test_more_items_than_the_gpu_has_ctas(kind, H, N, wide):
+    """200 sequences of 1 to 500 tokens (empty chunks among them): CTAs run through several items,
+    whole (a narrow table) or cut anywhere (a wide one)."""
+    m = bsa()
+    kv = [1 + (i * 37) % 500 for i in range(200)]
+    n_new = [min(N, k, 1 + i % (N + 1)) if i % 7 else 0 for i, k in enumerate(kv)]
+    c, oc = build(kind, 2, 16, 64, kv, 30, max_pages=200 if wide else 32)
+    q = _rand((200, H, N, 64), 31)
+    o = _forward(c, q, n_new, True, 0)
+    assert m.get_device_error() == 0
+    check_attention(o, q, oc, n_new, True, 0, 64 ** -0.5)
+    for b in range(200):
+        assert (o[b, :, n_new[b]:] == -3.0).all()
+
+
+def test_offsets_past_32_bits():
+    """Caches of more than 2^31 values (and bytes): the sequence's pages lie at the very end."""
+    m = bsa()
+    n_pages, Hkv, page, d = 2100, 8, 1024, 128                  # 2.2e9 codes each
+    g = torch.Generator(device="cuda").manual_seed(1)
+    code = lambda: torch.empty((n_pages, Hkv, page, d), dtype=torch.uint8, device="cuda")
+    c = m.PagedCache(code(), code(), _i32([[n_pages - 1, n_pages - 2]]), _i32([1500]),
+                     *(torch.ones((n_pages, Hkv, page), device="cuda") for _ in range(2)))
+    k, v = (torch.randn((1, Hkv, 1500, d), generator=g, device="cuda").bfloat16() for _ in range(2))
+    m.paged_append(m.dims(1, Hkv, 1500, d, 1, 1, 0), c, k, v)
+    rk, rv = torch.empty_like(k), torch.empty_like(v)
+    m.paged_read(m.dims(1, Hkv, 1500, d, 1, 1, 0), c, rk, rv)
+    oc = {"table": np.array([[0, 1]]), "kv_len": np.array([1500]), "page": page, "k": np.zeros((2, Hkv, page, d)),
+          "v": np.zeros((2, Hkv, page, d))}
+    vals = []
+    for x, r in ((k, rk), (v, rv)):
+        code_, s = OPG.quantize_tokens(x.float().cpu().numpy())
+        vals.append(code_ * s[..., None])
+        assert torch.equal(r.cpu(), torch.from_numpy((code_.astype(np.float32) * s.astype(np.float32)[..., None])).bfloat16())
+    oc = OPG.append(oc, *vals, [1500])
+    for N in (1, 40, 200):
+        q = _rand((1, Hkv, N, d), N)
+        check_attention(_forward(c, q, None, True, 0), q, oc, [N], True, 0, d ** -0.5)
+    assert m.get_device_error() == 0
+
+
+@pytest.mark.parametrize("N", [1, 40, 200])
+def test_a_token_that_is_not_finite_reaches_only_its_own_sequence(N):
+    """e4m3: a token with an infinity in K and V, appended mid-sequence: every row of that sequence
+    that keeps it is NaN, the other sequence's rows are as before."""
+    m = bsa()
+    kv = [300 + N, 400 + N]
+    c, _ = build(E4M3, 2, 16, 128, kv, 12)
+    q = _rand((2, 4, N, 128), 13)
+    good = _forward(c, q, None, True, 0)
+    pg = int(c.table[0, 100 // 16])
+    c.k_scale[pg, :, 100 % 16] = float("nan")
+    c.v_scale[pg, :, 100 % 16] = float("nan")
+    o = _forward(c, q, None, True, 0)
+    assert o[0].isnan().all() and torch.equal(o[1], good[1])
+    assert torch.equal(_forward(c, q, None, True, 64)[0].isnan(), torch.zeros_like(o[0], dtype=torch.bool))
+    assert m.get_device_error() == 0
+
+
+def test_sequences_may_share_pages():
+    """Two sequences with the same prompt pages and a page of their own each."""
+    m = bsa()
+    c, oc = build(BF16, 2, 16, 64, [64, 80], 14)
+    c.table[1, :3] = c.table[0, :3]
+    oc["table"][1, :3] = oc["table"][0, :3]
+    q = _rand((2, 4, 10, 64), 15)
+    check_attention(_forward(c, q, None, True, 0), q, oc, [10, 10], True, 0, 64 ** -0.5)
+    assert m.get_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", [BF16, E4M3])
+@pytest.mark.parametrize("H,Hkv,N,kv", [(4, 1, 1, 4000), (2, 1, 40, 6000), (1, 1, 300, 9000)])
+def test_a_wait_that_runs_out_is_reported_and_the_context_survives(kind, H, Hkv, N, kv):
+    """The producer withholds a CTA's second key tile and waits are bounded by 2 ms: the call ends
+    with BSA_DEVERR_TIMEOUT, and the next one is right."""
+    m = bsa()
+    c, oc = build(kind, Hkv, 64, 128, [kv, kv - 100], 16)
+    q = _rand((2, H, N, 128), 17)
+    good = _forward(c, q, None, True, 0)
+    assert m.get_device_error() == 0
+    m.set_wait_limit_ns(2_000_000)
+    m.set_withheld_tile(1)
+    try:
+        _forward(c, q, None, True, 0)
+        assert m.get_device_error() == m.DEVERR_TIMEOUT
+    finally:
+        m.set_withheld_tile(-1)
+        m.set_wait_limit_ns(0)
+    assert torch.equal(_forward(c, q, None, True, 0), good)
+    assert m.get_device_error() == 0
 
 
 @pytest.mark.parametrize("kind", [BF16, E4M3])
