@@ -484,6 +484,52 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
           const int nw = flush ? 0 : need.mask(kt);
           if (nw == 0 && !flush) continue;
           const int st = k % SK;
+          if constexpr (!E4M3 && !SPLIT) {
+            // The long run of tiles both row tiles need, each with its PV of
+            // the tile before outstanding: the same steps without the
+            // bookkeeping, which otherwise takes the issuer longer between two
+            // products than the tensor pipe has work queued
+            if (nw == 3 && cur.pt == k - 1 && oth.pt == k - 1 && !cur.fresh && !oth.fresh) {
+              const int n = min(need.e0, need.e1) - kt;  // such tiles from here on, at least this one
+              int ks = st, kp = (k / SK) & 1, vs = (k - 1) % SV, vp = ((k - 1) / SV) & 1;
+#pragma unroll 1
+              for (int x = 0; x < n && ok; ++x) {
+                const uint64_t vd = smem_desc_sw128(sVa + vs * C::VTILE, C::CHUNK, 1024);
+                const uint64_t kd = smem_desc_sw128(sKa + ks * C::KTILE, 16, 1024);
+                ok = wait(&k_full[ks], kp) && wait(&v_full[vs], vp);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                  ok = ok && wait(&p_full[w], w ? oth.np : cur.np);
+                  if (!ok) break;
+                  tc_fence_after();
+                  pv_halves(tmem + 256 + w * D, tmem + 128 * w, vd, idesc_pv, 0u, std::make_integer_sequence<int, 8>{});
+                  if (w) tc_commit_warp(&v_empty[vs]);
+                  qk_all(tmem + 128 * w, smem_desc_sw128(sQa + w * C::QTILE, 16, 1024), kd, idesc_qk,
+                         std::make_integer_sequence<int, D / 16>{});
+                  tc_commit_warp(&s_full[w]);
+                }
+                tc_commit_warp(&k_empty[ks]);
+                ++cur.np;
+                ++oth.np;
+                if (++ks == SK) {
+                  ks = 0;
+                  kp ^= 1;
+                }
+                if (++vs == SV) {
+                  vs = 0;
+                  vp ^= 1;
+                }
+              }
+              k += n;
+              v_seen = k - 1;
+              rem = 2u << (2 * ((k - 1) % SV));
+              cur.pt = oth.pt = k - 1;
+              cur.last = kt + n == need.e0;
+              oth.last = kt + n == need.e1;
+              i += n - 1;
+              continue;
+            }
+          }
           if (!flush)
             ok = wait(&k_full[st], k / SK);
           else
