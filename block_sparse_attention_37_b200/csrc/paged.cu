@@ -1,9 +1,11 @@
 // Writing the paged key/value cache and reading it back: one pass over the
 // chunk, bound by the bytes it reads and writes.
 //
-// A row is one token of one key/value head, d values. d / 8 lanes hold a row,
-// eight values (16 bytes of bf16) a lane, K's and V's row of a token side by
-// side in the same lanes, so the page lookup is paid once for both. The rows
+// A row is one token of one key/value head, d values, held by d / 8 lanes
+// (bf16) or d / 16 (e4m3: the copies are short, and finding a row's page and
+// converting it would otherwise take more issue slots than the bytes take
+// time), K's and V's row of a token side by side in the same lanes, so the page
+// lookup is paid once for both. The rows
 // of the [B, Hkv, N, d] tensor are numbered flat: a block of consecutive rows
 // is contiguous in the tensor and, page by page, in the cache, and a decode
 // step's single tokens fill blocks as well as a long prompt does.
@@ -59,143 +61,126 @@ __device__ __forceinline__ uint2 dequant4(uint32_t w, float s) {
   return make_uint2(pack_bf16x2(e.x * s, o.x * s), pack_bf16x2(e.y * s, o.y * s));
 }
 
-// U: rows a lane group keeps in flight (see launch_copy_any).
-template <int D, bool E4M3, int U>
+template <int D, bool E4M3>
 __global__ void __launch_bounds__(256) paged_append_kernel(const PagedParams p) {
-  constexpr int LANES = D / 8;
-  constexpr int GROUPS = 256 / LANES;
+  constexpr int W = E4M3 ? 2 : 1;  // 16-byte units of bf16 a lane
+  constexpr int LANES = D / (8 * W), ROWS = 256 / LANES;
   const int grp = threadIdx.x / LANES, l = threadIdx.x % LANES;
   const long long rows = (long long)p.B * p.Hkv * p.N;
-  const long long r0 = (long long)blockIdx.x * (GROUPS * U) + grp;
-  uint4 k[U], v[U];
-  long long dst[U];
+  const long long r = (long long)blockIdx.x * ROWS + grp;
+  uint4 k[W], v[W];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const long long r = r0 + u * GROUPS;
-    dst[u] = -1;
-    k[u] = v[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (r >= rows) continue;
+  for (int w = 0; w < W; ++w) k[w] = v[w] = make_uint4(0u, 0u, 0u, 0u);
+  long long dst = -1;
+  if (r < rows) {
     const int bh = fdiv((int)r, p.f_n), n = (int)r - bh * p.N;
     const int b = fdiv(bh, p.f_hkv), hk = bh - b * p.Hkv;
     const SeqLen s = seq_lens(p, b);
-    if (n >= s.n) continue;
-    k[u] = __ldg(reinterpret_cast<const uint4*>(p.new_k) + r * LANES + l);
-    v[u] = __ldg(reinterpret_cast<const uint4*>(p.new_v) + r * LANES + l);
-    const int j = s.kv - s.n + n;
-    if (j < 0) {
-      record_error(BSA_DEVERR_BAD_INDEX);
-      continue;
+    if (n < s.n) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        k[w] = __ldg(reinterpret_cast<const uint4*>(p.new_k) + (r * LANES + l) * W + w);
+        v[w] = __ldg(reinterpret_cast<const uint4*>(p.new_v) + (r * LANES + l) * W + w);
+      }
+      const int j = s.kv - s.n + n;
+      if (j < 0) {
+        record_error(BSA_DEVERR_BAD_INDEX);
+      } else {
+        const int pg = page_of(p, b, j);
+        if (pg >= 0) dst = cache_row(p, pg, hk, j);
+      }
     }
-    const int pg = page_of(p, b, j);
-    if (pg >= 0) dst[u] = cache_row(p, pg, hk, j);
   }
+  if constexpr (E4M3) {
+    uint32_t mk = max(amax_bits8(k[0]), amax_bits8(k[W - 1])), mv = max(amax_bits8(v[0]), amax_bits8(v[W - 1]));
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if constexpr (E4M3) {
-      uint32_t mk = amax_bits8(k[u]), mv = amax_bits8(v[u]);
-#pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) {
-        mk = max(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-        mv = max(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-      }
-      if (dst[u] < 0) continue;
-      float sk, rk, sv, rv;
-      row_scale(mk, sk, rk);
-      row_scale(mv, sv, rv);
-      // a row that is not finite holds zero codes under its NaN scale
-      const uint2 ck = rk == 0.f ? make_uint2(0u, 0u) : row_codes8(k[u], rk);
-      const uint2 cv = rv == 0.f ? make_uint2(0u, 0u) : row_codes8(v[u], rv);
-      reinterpret_cast<uint2*>(p.k)[dst[u] * LANES + l] = ck;
-      reinterpret_cast<uint2*>(p.v)[dst[u] * LANES + l] = cv;
-      if (l == 0) {
-        p.k_scale[dst[u]] = sk;
-        p.v_scale[dst[u]] = sv;
-      }
-    } else {
-      if (dst[u] < 0) continue;
-      reinterpret_cast<uint4*>(p.k)[dst[u] * LANES + l] = k[u];
-      reinterpret_cast<uint4*>(p.v)[dst[u] * LANES + l] = v[u];
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+      mk = max(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+      mv = max(mv, __shfl_xor_sync(0xffffffffu, mv, o));
     }
+    if (dst < 0) return;
+    float sk, rk, sv, rv;
+    row_scale(mk, sk, rk);
+    row_scale(mv, sv, rv);
+    const uint2 k0 = row_codes8(k[0], rk), k1 = row_codes8(k[W - 1], rk);
+    const uint2 v0 = row_codes8(v[0], rv), v1 = row_codes8(v[W - 1], rv);
+    // a row that is not finite holds zero codes under its NaN scale
+    reinterpret_cast<uint4*>(p.k)[dst * LANES + l] = rk == 0.f ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(k0.x, k0.y, k1.x, k1.y);
+    reinterpret_cast<uint4*>(p.v)[dst * LANES + l] = rv == 0.f ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(v0.x, v0.y, v1.x, v1.y);
+    if (l == 0) {
+      p.k_scale[dst] = sk;
+      p.v_scale[dst] = sv;
+    }
+  } else {
+    if (dst < 0) return;
+    reinterpret_cast<uint4*>(p.k)[dst * LANES + l] = k[0];
+    reinterpret_cast<uint4*>(p.v)[dst * LANES + l] = v[0];
   }
 }
 
-template <int D, bool E4M3, int U>
+template <int D, bool E4M3>
 __global__ void __launch_bounds__(256) paged_read_kernel(const PagedParams p) {
-  constexpr int LANES = D / 8;
-  constexpr int GROUPS = 256 / LANES;
+  constexpr int W = E4M3 ? 2 : 1;
+  constexpr int LANES = D / (8 * W), ROWS = 256 / LANES;
   const int grp = threadIdx.x / LANES, l = threadIdx.x % LANES;
   const long long rows = (long long)p.B * p.Hkv * p.N;
-  const long long r0 = (long long)blockIdx.x * (GROUPS * U) + grp;
-  long long src[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const long long r = r0 + u * GROUPS;
-    src[u] = -1;
-    if (r >= rows) continue;
-    const int bh = fdiv((int)r, p.f_n), n = (int)r - bh * p.N;
-    const int b = fdiv(bh, p.f_hkv), hk = bh - b * p.Hkv;
-    int kv = __ldg(p.kv_len + b);
-    int first = p.begin ? __ldg(p.begin + b) : 0;
-    const SeqLen s = clamp_lens(p, 0, kv);
-    if (s.bad || first < 0) record_error(BSA_DEVERR_BAD_INDEX);
-    const long long j = (long long)max(first, 0) + n;
-    if (j >= s.kv) continue;
+  const long long r = (long long)blockIdx.x * ROWS + grp;
+  if (r >= rows) return;
+  const int bh = fdiv((int)r, p.f_n), n = (int)r - bh * p.N;
+  const int b = fdiv(bh, p.f_hkv), hk = bh - b * p.Hkv;
+  const int first = p.begin ? __ldg(p.begin + b) : 0;
+  const SeqLen s = clamp_lens(p, 0, __ldg(p.kv_len + b));
+  if (s.bad || first < 0) record_error(BSA_DEVERR_BAD_INDEX);
+  const long long j = (long long)max(first, 0) + n;
+  long long src = -1;
+  if (j < s.kv) {
     const int pg = page_of(p, b, (int)j);
-    if (pg >= 0) src[u] = cache_row(p, pg, hk, (int)j);
+    if (pg >= 0) src = cache_row(p, pg, hk, (int)j);
   }
-  uint4 k[U], v[U];
+  uint4 k[W], v[W];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    k[u] = v[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (src[u] < 0) continue;
+  for (int w = 0; w < W; ++w) k[w] = v[w] = make_uint4(0u, 0u, 0u, 0u);
+  if (src >= 0) {
     if constexpr (E4M3) {
-      const uint2 ck = __ldg(reinterpret_cast<const uint2*>(p.k) + src[u] * LANES + l);
-      const uint2 cv = __ldg(reinterpret_cast<const uint2*>(p.v) + src[u] * LANES + l);
-      const float sk = __ldg(p.k_scale + src[u]), sv = __ldg(p.v_scale + src[u]);
-      const uint2 k0 = dequant4(ck.x, sk), k1 = dequant4(ck.y, sk);
-      const uint2 v0 = dequant4(cv.x, sv), v1 = dequant4(cv.y, sv);
-      k[u] = make_uint4(k0.x, k0.y, k1.x, k1.y);
-      v[u] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+      // eight codes of each half row: a lane's stores lie side by side with its
+      // neighbours' (16 codes in a row: 86 us for 407 MB, against 65)
+      const float sk = __ldg(p.k_scale + src), sv = __ldg(p.v_scale + src);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const uint2 ck = __ldg(reinterpret_cast<const uint2*>(p.k) + (src * W + w) * LANES + l);
+        const uint2 cv = __ldg(reinterpret_cast<const uint2*>(p.v) + (src * W + w) * LANES + l);
+        const uint2 k0 = dequant4(ck.x, sk), k1 = dequant4(ck.y, sk);
+        const uint2 v0 = dequant4(cv.x, sv), v1 = dequant4(cv.y, sv);
+        k[w] = make_uint4(k0.x, k0.y, k1.x, k1.y);
+        v[w] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+      }
     } else {
-      k[u] = __ldg(reinterpret_cast<const uint4*>(p.k) + src[u] * LANES + l);
-      v[u] = __ldg(reinterpret_cast<const uint4*>(p.v) + src[u] * LANES + l);
+      k[0] = __ldg(reinterpret_cast<const uint4*>(p.k) + src * LANES + l);
+      v[0] = __ldg(reinterpret_cast<const uint4*>(p.v) + src * LANES + l);
     }
   }
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const long long r = r0 + u * GROUPS;
-    if (r >= rows) continue;
-    reinterpret_cast<uint4*>(p.new_k)[r * LANES + l] = k[u];
-    reinterpret_cast<uint4*>(p.new_v)[r * LANES + l] = v[u];
+  for (int w = 0; w < W; ++w) {
+    reinterpret_cast<uint4*>(p.new_k)[(r * W + w) * LANES + l] = k[w];
+    reinterpret_cast<uint4*>(p.new_v)[(r * W + w) * LANES + l] = v[w];
   }
 }
 
-template <int D, bool E4M3, int U>
+template <int D, bool E4M3>
 static cudaError_t launch_copy(bool append, const PagedParams& p, cudaStream_t stream) {
-  const long long per = 256 / (D / 8) * U;
+  const long long per = 256 / (D / (E4M3 ? 16 : 8));
   const long long rows = (long long)p.B * p.Hkv * p.N;
   const unsigned grid = (unsigned)((rows + per - 1) / per);
   if (append)
-    paged_append_kernel<D, E4M3, U><<<grid, 256, 0, stream>>>(p);
+    paged_append_kernel<D, E4M3><<<grid, 256, 0, stream>>>(p);
   else
-    paged_read_kernel<D, E4M3, U><<<grid, 256, 0, stream>>>(p);
+    paged_read_kernel<D, E4M3><<<grid, 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
-// bf16 rows are long enough to fill the memory pipe one a lane group (append of
-// 211 MB: 33.6 us with one, 34.2 with two, against 32.6 at the copy bandwidth).
-// e4m3 rows have fewer bytes and more between load and store: two, once there
-// are rows for every SM (209 MB: 52.4 us with two, 53.9 with one, 57.1 with
-// four); one keeps a decode step's 512 rows spread wider (2.2 us against 3.0).
-template <int D>
-static cudaError_t launch_copy_d(bool append, const PagedParams& p, cudaStream_t stream) {
-  if (!p.e4m3) return launch_copy<D, false, 1>(append, p, stream);
-  if ((long long)p.B * p.Hkv * p.N < 65536) return launch_copy<D, true, 1>(append, p, stream);
-  return launch_copy<D, true, 2>(append, p, stream);
-}
-
 static cudaError_t launch_copy_any(bool append, const PagedParams& p, cudaStream_t stream) {
-  return p.d == 64 ? launch_copy_d<64>(append, p, stream) : launch_copy_d<128>(append, p, stream);
+  if (p.d == 64) return p.e4m3 ? launch_copy<64, true>(append, p, stream) : launch_copy<64, false>(append, p, stream);
+  return p.e4m3 ? launch_copy<128, true>(append, p, stream) : launch_copy<128, false>(append, p, stream);
 }
 
 cudaError_t launch_paged_append(const PagedParams& p, cudaStream_t stream) { return launch_copy_any(true, p, stream); }
