@@ -341,8 +341,9 @@ size_t bsa_paged_workspace_size(const bsa_dims* dims, const bsa_paged_cache* cac
  *  causal = 0: every key j < kv_len[b];
  *  causal = 1: the keys j <= p, and of these, with window > 0, j > p - window.
  *  o = softmax(scale * q.k) V over the kept keys, fp32 accumulation, the
- *  weights rounded to bf16 for the product with V, o rounded to bf16; a row
- *  that keeps no key gives 0. Rows i >= n_new[b] of O are left as they were.
+ *  weights rounded to 16 bits for the product with V (bf16; fp16 for an e4m3
+ *  cache, whose codes and K scales enter unrounded), o rounded to bf16;
+ *  a row that keeps no key gives 0. Rows i >= n_new[b] of O are left as they were.
  *  dims: B, H, N and d are read. Q, O: device bf16 [B, H, N, d].
  *  window: 0 for none; needs causal = 1. scale: finite and positive.
  *  workspace: device, at least bsa_paged_workspace_size bytes, 256-byte

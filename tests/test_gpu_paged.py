@@ -458,6 +458,66 @@ def test_two_graphs_and_a_side_stream():
     assert m.get_device_error() == 0
 
 
+@pytest.mark.parametrize("H,N", [(8, 1), (4, 40), (4, 200)])
+def test_a_call_captured_behind_copies_and_a_fork(H, N):
+    """The queries arrive by a copy node, the cache by a kernel on a forked stream: the captured call
+    waits for both, replay after replay, with new queries and new keys each time."""
+    m = bsa()
+    kv = 1500
+    c, oc = build(BF16, 2, 64, 128, [kv], 50, max_pages=64)
+    dm = m.dims(1, H, N, 128, 1, 1, 0)
+    ws = torch.empty(m.paged_workspace_size(dm, c), dtype=torch.uint8, device="cuda")
+    src, q = (torch.zeros((1, H, N, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k, v = (torch.zeros((1, 2, N, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    o = torch.zeros_like(q)
+    m.paged_forward(dm, c, q, o, ws)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            m.paged_append(dm, c, k, v)
+        q.copy_(src)
+        main.wait_stream(side)
+        m.paged_forward(dm, c, q, o, ws)
+        q.copy_(src)
+        m.paged_forward(dm, c, q, o, ws)
+    for seed in range(3):
+        hk, hv, hq = _rand((1, 2, N, 128), seed), _rand((1, 2, N, 128), 10 + seed), _rand((1, H, N, 128), 20 + seed)
+        k.copy_(hk)
+        v.copy_(hv)
+        src.copy_(hq)
+        oc = OPG.append(oc, hk.double().numpy(), hv.double().numpy(), [N])
+        gr.replay()
+        torch.cuda.synchronize()
+        check_attention(o, hq, oc, [N], True, 0, 128 ** -0.5, f"replay {seed}")
+    assert m.get_device_error() == 0
+
+
+def test_two_streams_at_once():
+    """Calls of both kernels on two streams, a workspace each, launched without waiting: as alone."""
+    m = bsa()
+    work = []
+    for i, (H, N) in enumerate([(8, 1), (4, 300)]):
+        c, _ = build(E4M3 if i else BF16, 2, 16, 128, [3000 + N, 40 + N], 60 + i, garbage=0.5)
+        q = _rand((2, H, N, 128), 70 + i).cuda()
+        dm = m.dims(2, H, N, 128, 1, 1, 0)
+        ws = torch.empty(m.paged_workspace_size(dm, c), dtype=torch.uint8, device="cuda")
+        o = torch.zeros_like(q)
+        m.paged_forward(dm, c, q, o, ws)
+        work.append((dm, c, q, o, ws, o.clone(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for dm, c, q, o, ws, want, st in work:
+            m.paged_forward(dm, c, q, o, ws, stream=st)
+    torch.cuda.synchronize()
+    for dm, c, q, o, ws, want, st in work:
+        assert torch.equal(o, want)
+    assert m.get_device_error() == 0
+
+
 @pytest.mark.parametrize("N", [1, 30, 140])
 @pytest.mark.parametrize("kind", [BF16, E4M3])
 def test_faults_are_reported_and_the_next_call_is_right(kind, N):
