@@ -93,6 +93,13 @@ PagedCut paged_cut(const PagedParams& p) {
   c.keys = c.rows == 16 ? 64 : 128;
   c.row_tiles = ceil_div(rows, c.rows);
   c.grid = (c.rows == 16 ? 2 : 1) * num_sms();
+  // Few items of many rows: as many CTAs as give each item the same number, so
+  // that items of one length are cut into whole runs and no CTA fills its
+  // pipeline for two (32 items of 32 tiles: 27.6 us with 128 CTAs, 31.6 with
+  // 148). From two CTAs an item on the idle SMs cost as much; the few-rows
+  // kernel is bound by HBM and keeps every CTA.
+  const long long items = (long long)p.B * p.Hkv * c.row_tiles;
+  if (c.rows != 16 && 4 * items <= c.grid) c.grid = (int)(c.grid / items * items);
   return c;
 }
 

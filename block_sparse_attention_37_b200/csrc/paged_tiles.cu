@@ -1055,6 +1055,76 @@ __global__ void __launch_bounds__(256) paged_join_tiles_kernel(const PagedParams
         make_uint2(pack_bf16x2(acc[c].x * inv, acc[c].y * inv), pack_bf16x2(acc[c].z * inv, acc[c].w * inv));
 }
 
+// The same for few items, whose parts are many: grid (CTAs of the forward,
+// ROWS / 32 * D / 16), a block 32 rows and four groups of four channels, its
+// eight warps sharing the parts (one item in 40 parts: 23 us the other way).
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256) paged_join_parts_kernel(const PagedParams p, const PagedWork wk, int row_tiles) {
+  __shared__ float4 acc_sh[8][4][32];
+  __shared__ float2 ml_sh[8][32];
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const SplitItem it = wk.split[blockIdx.x];
+  if (it.parts <= 1) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = it.idx / row_tiles, rt = it.idx - b * row_tiles;
+  const SeqLen s = clamp_lens(p, p.n_new ? __ldg(p.n_new + b) : p.N, __ldg(p.kv_len + b));
+  const int r = (blockIdx.y % (ROWS / 32)) * 32 + lane, c0 = blockIdx.y / (ROWS / 32) * 4;
+  const int R = rt * ROWS + r;
+  const bool written = R < p.G * p.N && R - fdiv(R, p.f_n) * p.N < s.n;
+  if (!__any_sync(0xffffffffu, written)) return;  // the same rows in every warp of the block
+  auto slot = [&](int i) -> size_t { return i == 0 ? 2 * (size_t)blockIdx.x + 1 : 2 * ((size_t)blockIdx.x + i); };
+  // each warp's own parts against their own maximum, then the warps' sums
+  float m = kNegInf, l = 0.f;
+  if (written)
+#pragma unroll 8
+    for (int i = warp; i < it.parts; i += 8) m = fmaxf(m, wk.ml[slot(i) * ROWS + r].x);
+  const float mu = m == kNegInf ? 0.f : m;
+  float4 acc[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (written)
+#pragma unroll 4
+    for (int i = warp; i < it.parts; i += 8) {
+      const float2 ml = wk.ml[slot(i) * ROWS + r];
+      const float4* o = reinterpret_cast<const float4*>(wk.o) + (slot(i) * (D / 4) + c0) * ROWS + r;
+      const float e = fast_exp2(ml.x - mu);
+      l += ml.y * e;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 v = o[c * ROWS];
+        acc[c].x += v.x * e;
+        acc[c].y += v.y * e;
+        acc[c].z += v.z * e;
+        acc[c].w += v.w * e;
+      }
+    }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) acc_sh[warp][c][lane] = acc[c];
+  ml_sh[warp][lane] = make_float2(m, l);
+  __syncthreads();
+  if (warp >= 4 || !written) return;  // warp c finishes channel group c
+  float M = kNegInf;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) M = fmaxf(M, ml_sh[w][lane].x);
+  const float Mu = M == kNegInf ? 0.f : M;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const float e = fast_exp2(ml_sh[w][lane].x - Mu);
+    const float4 v = acc_sh[w][warp][lane];
+    x.x += v.x * e;
+    x.y += v.y * e;
+    x.z += v.z * e;
+    x.w += v.w * e;
+    l += ml_sh[w][lane].y * e;
+  }
+  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+  *reinterpret_cast<uint2*>(p.O + ((size_t)(b * p.Hkv + it.hk) * p.G * p.N + R) * D + 4 * (c0 + warp)) =
+      make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+}
+
 template <int D, bool E4M3, bool SPLIT>
 static cudaError_t launch_tiles_d(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                                   const PagedParams& p, const PagedWork& w, int row_tiles, int grid,
@@ -1071,6 +1141,8 @@ static cudaError_t launch_tiles_d(const CUtensorMap& q, const CUtensorMap& k, co
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (p.whole_items) return cudaSuccess;
   constexpr int ROWS = SPLIT ? 128 : 256;
+  if ((long long)p.B * p.Hkv * row_tiles * 8 <= grid)  // eight parts an item, or more
+    return launch_after(paged_join_parts_kernel<D, ROWS>, dim3(grid, ROWS / 32 * (D / 16)), 256, 0, stream, p, w, row_tiles);
   return launch_after(paged_join_tiles_kernel<D, ROWS>, dim3(grid, 8), 256, 0, stream, p, w, row_tiles);
 }
 
