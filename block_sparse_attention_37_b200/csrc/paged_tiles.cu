@@ -9,8 +9,8 @@
 // tensor core still has two independent softmaxes to work between. Either way
 // it runs one row tile's PV and next QK^T under the other's softmax. A row
 // tile's softmax is two warpgroups, each half of the columns: a tile's chain
-// QK^T - softmax - PV is what a row tile waits for, and eight warps pass
-// through it in half the time of four.
+// QK^T - softmax - PV is what a row tile waits for, and eight warps shorten
+// it (one warpgroup each: causal chunk 972 us, two: 943).
 // Roles:
 //   warp 0      TMA producer of K (a lane a copy: a page's part of a tile)
 //   warp 1      TMEM allocator and tcgen05.mma issuer
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
   if (tid == 0) {
     for (int w = 0; w < 2; ++w) {
       mbar_init(&q_full[w], 1);
-      mbar_init(&q_ready[w], 8);  // one arrival a warp: 256 on one barrier queue for longer than the softmax
+      mbar_init(&q_ready[w], 8);  // (an arrival a warp)
       mbar_init(&s_full[w], 1);
       mbar_init(&p_full[w], 8);
       mbar_init(&o_ready[w], 1);
