@@ -63,6 +63,8 @@ __device__ __forceinline__ uint2 dequant4(uint32_t w, float s) {
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(256) paged_append_kernel(const PagedParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // before any read or write
   constexpr int W = E4M3 ? 2 : 1;  // 16-byte units of bf16 a lane
   constexpr int LANES = D / (8 * W), ROWS = 256 / LANES;
   const int grp = threadIdx.x / LANES, l = threadIdx.x % LANES;
@@ -120,6 +122,8 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const PagedParams p) 
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(256) paged_read_kernel(const PagedParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // before any read or write
   constexpr int W = E4M3 ? 2 : 1;
   constexpr int LANES = D / (8 * W), ROWS = 256 / LANES;
   const int grp = threadIdx.x / LANES, l = threadIdx.x % LANES;
@@ -171,11 +175,8 @@ static cudaError_t launch_copy(bool append, const PagedParams& p, cudaStream_t s
   const long long per = 256 / (D / (E4M3 ? 16 : 8));
   const long long rows = (long long)p.B * p.Hkv * p.N;
   const unsigned grid = (unsigned)((rows + per - 1) / per);
-  if (append)
-    paged_append_kernel<D, E4M3><<<grid, 256, 0, stream>>>(p);
-  else
-    paged_read_kernel<D, E4M3><<<grid, 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return append ? launch_after(paged_append_kernel<D, E4M3>, dim3(grid), 256, 0, stream, p)
+                : launch_after(paged_read_kernel<D, E4M3>, dim3(grid), 256, 0, stream, p);
 }
 
 static cudaError_t launch_copy_any(bool append, const PagedParams& p, cudaStream_t stream) {

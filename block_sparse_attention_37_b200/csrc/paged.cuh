@@ -85,6 +85,25 @@ __host__ __device__ __forceinline__ long long cache_row(const PagedParams& p, in
   return (((long long)pg * p.Hkv + hk) << p.page_log2) + (j & ((1 << p.page_log2) - 1));
 }
 
+#ifdef __CUDACC__
+// A launch that may be scheduled while the kernel before it finishes; every
+// kernel launched so waits (griddepcontrol.wait) before it reads memory.
+template <class K, class... A>
+static cudaError_t launch_after(K kernel, dim3 grid, unsigned block, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#endif
+
 cudaError_t launch_paged_append(const PagedParams& p, cudaStream_t stream);
 cudaError_t launch_paged_read(const PagedParams& p, cudaStream_t stream);
 struct PagedWork;

@@ -645,23 +645,6 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, co
   }
 }
 
-// A launch that may be scheduled while the kernel before it finishes; every
-// kernel launched so waits (griddepcontrol.wait) before it reads memory.
-template <class K, class... A>
-static cudaError_t launch_after(K kernel, dim3 grid, unsigned block, size_t smem, cudaStream_t stream, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int D, bool E4M3, int R8, int NG>
 static cudaError_t launch_rows_d(const CUtensorMap& k, const CUtensorMap& v, const PagedParams& p, const PagedWork& w,
                                  int grid, cudaStream_t stream) {
