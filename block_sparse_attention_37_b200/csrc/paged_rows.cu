@@ -18,10 +18,11 @@
 //
 // e4m3: codes become fp16 in registers (exact). K's scale multiplies the
 // logit; V's, over sigma, the weight: sigma is a power of two, the largest V
-// scale the warp has met, so the weights stay in fp16's range, and O carries
-// 1 / sigma as it carries the running maximum. Weights are held times 2^12:
-// what fp16 flushes is below 2^-36 of the largest, and 11 bits of weight
-// round less than bf16's eight.
+// scale the warp has met of a token that is not all zeros, so the weights stay
+// in fp16's range, and O carries 1 / sigma as it carries the running maximum.
+// Weights are held times 2^12: what fp16 flushes of (weight times V scale) is
+// below 2^-36 of the largest V scale, and 11 bits of weight round less than
+// bf16's eight.
 #include "paged_sched.cuh"
 #include "tiles.cuh"
 
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
       m[i] = kNegInf;
       mu[i] = l[i] = 0.f;
     }
-    // e4m3: a power of two, at least every finite V scale so far, and gain / sigma
+    // e4m3: a power of two, at least every finite V scale of a token with values so far, and gain / sigma
     float sigma = 0x1p-112f, rs = kRowsGain / 0x1p-112f;
 
     // the group's tiles: every NG-th of the run
@@ -397,6 +398,29 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
           l[i] *= alpha[i];
         }
         if constexpr (E4M3) {
+          // A token of zeros adds nothing whatever its scale (1, as it is
+          // written): it must not move sigma, above which V's weights would
+          // sink into fp16's subnormals, and its own weight must stay finite.
+          // Four lanes read a key's codes; only scales above sigma need it.
+          if (__any_sync(0xffffffffu, fmaxf(v0, v1) > sigma)) {
+            const uint32_t lin = (16 * w4 + g) * D + t4 * (D / 4);
+            const uint32_t at = vb + (lin ^ ((lin >> 3) & 0x70u));
+            uint32_t z0 = 0u, z1 = 0u;
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+              uint32_t x[4], y[4];
+              lds128(x, at ^ (16 * h));
+              lds128(y, D == 64 ? (at + 512) ^ 64 : (at + 1024) ^ (16 * h));
+              z0 |= x[0] | x[1] | x[2] | x[3];
+              z1 |= y[0] | y[1] | y[2] | y[3];
+            }
+            z0 |= __shfl_xor_sync(0xffffffffu, z0, 1);
+            z1 |= __shfl_xor_sync(0xffffffffu, z1, 1);
+            z0 |= __shfl_xor_sync(0xffffffffu, z0, 2);
+            z1 |= __shfl_xor_sync(0xffffffffu, z1, 2);
+            if (v0 > sigma && (z0 & 0x7f7f7f7fu) == 0u) v0 = 0.f;
+            if (v1 > sigma && (z1 & 0x7f7f7f7fu) == 0u) v1 = 0.f;
+          }
           // the largest finite scale of the warp's keys, as bits
           const uint32_t b0 = __float_as_uint(v0), b1 = __float_as_uint(v1);
           const uint32_t top =

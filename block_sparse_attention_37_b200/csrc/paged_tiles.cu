@@ -27,11 +27,13 @@
 // values, its rounding and the rest, which hold bf16's eight bits exactly down
 // to 2^-9 of the row's largest value (2^-18 of it is the error below that), so
 // two products give the logits and take the time of one in bf16. K's scale
-// multiplies the logits. PV runs in fp16: V is code * scale / sigma (sigma a
-// power of two, the largest V scale of the piece so far) rounded once to 11
-// bits, the weights fp16 times 2^12 (what is flushed is below 2^-36 of the
-// largest); O is rescaled when sigma grows. Weights in e4m3 would lose those
-// below 2^-18, which a long context's sum needs.
+// multiplies the logits. PV runs in fp16: V is code times (scale / sigma), the
+// quotient rounded to 11 bits and the product once more (sigma a power of two,
+// the largest V scale of the piece so far of a token that is not all zeros), the
+// weights fp16 times 2^12 (what is flushed is below 2^-36 of the largest); O is
+// rescaled when sigma grows. A scale below 2^-21 of sigma has fewer bits: the
+// quotient is then subnormal in fp16. Weights in e4m3 would lose those below
+// 2^-18, which a long context's sum needs.
 #include <type_traits>
 
 #include "mma_steps.cuh"
@@ -946,19 +948,48 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
               const int j4 = key0 + 4 * lane;
               const float4 f = reinterpret_cast<const float4*>(land)[lane];
               const float fs[4] = {f.x, f.y, f.z, f.w};
-              uint32_t top = 0u;
+              uint32_t b[4];  // as bits; 0 for what does not count
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const uint32_t b = __float_as_uint(fs[e]);
-                if (b < 0x7f800000u && (!edge || (j4 + e >= q.s.lo && j4 + e < q.s.hi))) top = max(top, b);
+                b[e] = __float_as_uint(fs[e]);
+                if (b[e] >= 0x7f800000u || (edge && (j4 + e < q.s.lo || j4 + e >= q.s.hi))) b[e] = 0u;
               }
-              top = __reduce_max_sync(0xffffffffu, top);
-              if (top > __float_as_uint(sig)) sig = __uint_as_float(min((top + 0x7fffffu) & 0x7f800000u, 0x7f000000u));
+              uint32_t top = __reduce_max_sync(0xffffffffu, max(max(b[0], b[1]), max(b[2], b[3])));
+              if (top > __float_as_uint(sig)) {
+                // A token of zeros adds nothing whatever its scale (1, as it
+                // is written): it must not move sigma, or V's small values
+                // would sink into fp16's subnormals. Of the tokens with the
+                // largest scale one must have a value, or the next largest
+                // scale is looked at; the second half's codes land first.
+                ok = wait(&raw_full[(c + 1) % C::RAW], (c + 1) / C::RAW);
+                while (ok && top > __float_as_uint(sig)) {
+                  const uint8_t* codes = smem + C::RAW_OFF + ((c + (lane >> 4)) % C::RAW) * C::RAW_BYTES;
+                  bool some = false;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    if (b[e] != top) continue;
+                    uint32_t any = 0u;
+#pragma unroll 1
+                    for (int u = 0; u < D / 16; ++u) {
+                      const uint32_t lin = (4 * (lane & 15) + e) * D + u * 16;
+                      const uint4 y = *reinterpret_cast<const uint4*>(codes + (lin ^ ((lin >> 3) & 0x70u)));
+                      any |= y.x | y.y | y.z | y.w;
+                    }
+                    if (any & 0x7f7f7f7fu)
+                      some = true;
+                    else
+                      b[e] = 0u;
+                  }
+                  if (__any_sync(0xffffffffu, some)) break;
+                  top = __reduce_max_sync(0xffffffffu, max(max(b[0], b[1]), max(b[2], b[3])));
+                }
+                if (top > __float_as_uint(sig)) sig = __uint_as_float(min((top + 0x7fffffu) & 0x7f800000u, 0x7f000000u));
+              }
               if (cw == 0 && lane == 0) {
                 *reinterpret_cast<float*>(smem + C::SIG_OFF + (k % C::R) * 4) = sig;
                 mbar_arrive(&sig_full[k % C::R]);
               }
-              if (k >= SV) ok = wait(&v_empty[st], k / SV - 1);
+              if (k >= SV) ok = ok && wait(&v_empty[st], k / SV - 1);
             }
             if (!ok) {
               cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
@@ -978,7 +1009,8 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
               uint32_t h[8] = {codes_lo(y.x), codes_hi(y.x), codes_lo(y.y), codes_hi(y.y),
                                codes_lo(y.z), codes_hi(y.z), codes_lo(y.w), codes_hi(y.w)};
               const int row = 64 * half + key;
-              const float s = land[row] * up;
+              const float f = land[row];  // (above sigma: a token of zeros; NaN stays)
+              const float s = (f > sig && f <= 3.402823466e38f ? sig : f) * up;
               const uint32_t s2 = pack_f16x2(s, s);
               // rows of no kept key are cleared: their codes and scales may be anything
               const bool out = edge && (key0 + row < q.s.lo || key0 + row >= q.s.hi);

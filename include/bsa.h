@@ -341,9 +341,17 @@ size_t bsa_paged_workspace_size(const bsa_dims* dims, const bsa_paged_cache* cac
  *  causal = 0: every key j < kv_len[b];
  *  causal = 1: the keys j <= p, and of these, with window > 0, j > p - window.
  *  o = softmax(scale * q.k) V over the kept keys, fp32 accumulation, the
- *  weights rounded to 16 bits for the product with V (bf16; fp16 for an e4m3
- *  cache, whose codes and K scales enter unrounded), o rounded to bf16;
+ *  weights rounded to 16 bits for the product with V, o rounded to bf16;
  *  a row that keeps no key gives 0. Rows i >= n_new[b] of O are left as they were.
+ *  What is rounded before the products: the weights, to bf16 (bf16 cache), or to
+ *  fp16 (e4m3 cache), there with the token's V scale (up to 16 rows a key/value
+ *  head) or beside V values rounded twice to 11 bits (more rows); and, for an e4m3
+ *  cache and more than 16 rows, Q: exact down to 2^-9 of its row's largest value,
+ *  with an error of 2^-18 of that value below. Codes and K scales are not.
+ *  V in an e4m3 cache is held over the largest V scale among the tokens of values
+ *  (not all zeros) that any row of the same tile keeps: tokens with V scales down
+ *  to 2^-20 of it keep their bits, smaller ones lose them, and where a weight
+ *  times the scale is below 2^-36 of it the token adds nothing.
  *  dims: B, H, N and d are read. Q, O: device bf16 [B, H, N, d].
  *  window: 0 for none; needs causal = 1. scale: finite and positive.
  *  workspace: device, at least bsa_paged_workspace_size bytes, 256-byte
