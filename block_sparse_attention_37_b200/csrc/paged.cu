@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const PagedParams p) 
     if (n < s.n) {
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        k[w] = __ldg(reinterpret_cast<const uint4*>(p.new_k) + (r * LANES + l) * W + w);
-        v[w] = __ldg(reinterpret_cast<const uint4*>(p.new_v) + (r * LANES + l) * W + w);
+        k[w] = reinterpret_cast<const uint4*>(p.new_k)[(r * LANES + l) * W + w];
+        v[w] = reinterpret_cast<const uint4*>(p.new_v)[(r * LANES + l) * W + w];
       }
       const int j = s.kv - s.n + n;
       if (j < 0) {
@@ -132,8 +132,8 @@ __global__ void __launch_bounds__(256) paged_read_kernel(const PagedParams p) {
   if (r >= rows) return;
   const int bh = fdiv((int)r, p.f_n), n = (int)r - bh * p.N;
   const int b = fdiv(bh, p.f_hkv), hk = bh - b * p.Hkv;
-  const int first = p.begin ? __ldg(p.begin + b) : 0;
-  const SeqLen s = clamp_lens(p, 0, __ldg(p.kv_len + b));
+  const int first = p.begin ? p.begin[b] : 0;
+  const SeqLen s = clamp_lens(p, 0, p.kv_len[b]);
   if (s.bad || first < 0) record_error(BSA_DEVERR_BAD_INDEX);
   const long long j = (long long)max(first, 0) + n;
   long long src = -1;
@@ -148,19 +148,19 @@ __global__ void __launch_bounds__(256) paged_read_kernel(const PagedParams p) {
     if constexpr (E4M3) {
       // eight codes of each half row: a lane's stores lie side by side with its
       // neighbours' (16 codes in a row: 86 us for 407 MB, against 65)
-      const float sk = __ldg(p.k_scale + src), sv = __ldg(p.v_scale + src);
+      const float sk = p.k_scale[src], sv = p.v_scale[src];
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const uint2 ck = __ldg(reinterpret_cast<const uint2*>(p.k) + (src * W + w) * LANES + l);
-        const uint2 cv = __ldg(reinterpret_cast<const uint2*>(p.v) + (src * W + w) * LANES + l);
+        const uint2 ck = reinterpret_cast<const uint2*>(p.k)[(src * W + w) * LANES + l];
+        const uint2 cv = reinterpret_cast<const uint2*>(p.v)[(src * W + w) * LANES + l];
         const uint2 k0 = dequant4(ck.x, sk), k1 = dequant4(ck.y, sk);
         const uint2 v0 = dequant4(cv.x, sv), v1 = dequant4(cv.y, sv);
         k[w] = make_uint4(k0.x, k0.y, k1.x, k1.y);
         v[w] = make_uint4(v0.x, v0.y, v1.x, v1.y);
       }
     } else {
-      k[0] = __ldg(reinterpret_cast<const uint4*>(p.k) + src * LANES + l);
-      v[0] = __ldg(reinterpret_cast<const uint4*>(p.v) + src * LANES + l);
+      k[0] = reinterpret_cast<const uint4*>(p.k)[src * LANES + l];
+      v[0] = reinterpret_cast<const uint4*>(p.v)[src * LANES + l];
     }
   }
 #pragma unroll

@@ -51,8 +51,24 @@ __host__ __device__ __forceinline__ SeqLen clamp_lens(const PagedParams& p, int 
   return s;
 }
 
+// Lengths and table entries. What the kernel before writes is not read-only
+// for the lifetime of a kernel launched as its dependent (launch_after), and
+// griddepcontrol.wait orders no load of the read-only path: such kernels read
+// by ordinary loads. READ_ONLY is for kernels launched the plain way.
+constexpr bool kReadOnly = true;
+template <bool READ_ONLY>
+__device__ __forceinline__ int load_i32(const int32_t* a) {
+  return READ_ONLY ? __ldg(a) : *a;
+}
+
+template <bool READ_ONLY = false>
+__device__ __forceinline__ SeqLen seq_clamped(const PagedParams& p, int b) {
+  return clamp_lens(p, p.n_new ? load_i32<READ_ONLY>(p.n_new + b) : p.N, load_i32<READ_ONLY>(p.kv_len + b));
+}
+
+template <bool READ_ONLY = false>
 __device__ __forceinline__ SeqLen seq_lens(const PagedParams& p, int b) {
-  const SeqLen s = clamp_lens(p, p.n_new ? __ldg(p.n_new + b) : p.N, __ldg(p.kv_len + b));
+  const SeqLen s = seq_clamped<READ_ONLY>(p, b);
   if (s.bad) record_error(BSA_DEVERR_BAD_INDEX);
   return s;
 }
@@ -60,7 +76,7 @@ __device__ __forceinline__ SeqLen seq_lens(const PagedParams& p, int b) {
 // The page of position j of sequence b (j inside the table's row); -1, with
 // the fault recorded, for an index outside the cache.
 __device__ __forceinline__ int page_of(const PagedParams& p, int b, int j) {
-  const int pg = __ldg(p.table + (size_t)b * p.max_pages + (j >> p.page_log2));
+  const int pg = p.table[(size_t)b * p.max_pages + (j >> p.page_log2)];
   if (pg < 0 || pg >= p.n_pages) {
     record_error(BSA_DEVERR_BAD_INDEX);
     return -1;
@@ -71,8 +87,9 @@ __device__ __forceinline__ int page_of(const PagedParams& p, int b, int j) {
 // The same in two steps, for producers that look a tile ahead: the entry is
 // read early and checked when the copy goes out; an index outside the cache
 // is recorded and page 0 read in its place.
+template <bool READ_ONLY = false>
 __device__ __forceinline__ int table_entry(const PagedParams& p, int b, int j) {
-  return __ldg(p.table + (size_t)b * p.max_pages + (j >> p.page_log2));
+  return load_i32<READ_ONLY>(p.table + (size_t)b * p.max_pages + (j >> p.page_log2));
 }
 __device__ __forceinline__ int checked_page(const PagedParams& p, int entry) {
   if (entry >= 0 && entry < p.n_pages) return entry;
@@ -87,7 +104,8 @@ __host__ __device__ __forceinline__ long long cache_row(const PagedParams& p, in
 
 #ifdef __CUDACC__
 // A launch that may be scheduled while the kernel before it finishes; every
-// kernel launched so waits (griddepcontrol.wait) before it reads memory.
+// kernel launched so waits (griddepcontrol.wait) before it reads memory, and
+// reads by ordinary loads (see load_i32).
 template <class K, class... A>
 static cudaError_t launch_after(K kernel, dim3 grid, unsigned block, size_t smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};

@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
           x[s] = make_uint2(0u, 0u);
-          if (have) x[s] = __ldg(reinterpret_cast<const uint2*>(src + 64 * (s >> 2) + 16 * t4 + 4 * (s & 3)));
+          if (have) x[s] = *reinterpret_cast<const uint2*>(src + 64 * (s >> 2) + 16 * t4 + 4 * (s & 3));
           const uint32_t u = __vmaxu2(x[s].x & 0x7fff7fffu, x[s].y & 0x7fff7fffu);
           top = max(top, max(u & 0xffffu, u >> 16));
         }
@@ -285,8 +285,8 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
       } else {
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
-          qf[e][s][0] = have ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * t4)) : 0u;
-          qf[e][s][1] = have ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 8 + 2 * t4)) : 0u;
+          qf[e][s][0] = have ? *reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * t4) : 0u;
+          qf[e][s][1] = have ? *reinterpret_cast<const uint32_t*>(src + 16 * s + 8 + 2 * t4) : 0u;
         }
         zs[2 * e] = zs[2 * e + 1] = p.scale_log2;
       }
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p, co
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = it.idx / row_tiles, rt = it.idx - b * row_tiles;
   const int rows = min(ROWS, p.G * p.N - rt * ROWS);
-  const SeqLen s = clamp_lens(p, p.n_new ? __ldg(p.n_new + b) : p.N, __ldg(p.kv_len + b));
+  const SeqLen s = seq_clamped(p, b);
   // part i: slot 2c + 1 of the first CTA, slot 2 (c + i) of the others
   auto slot = [&](int i) -> size_t { return i == 0 ? 2 * (size_t)blockIdx.x + 1 : 2 * ((size_t)blockIdx.x + i); };
   for (int r = blockIdx.y; r < rows; r += gridDim.y) {

@@ -116,7 +116,7 @@ __device__ __forceinline__ int line_tiles(const PagedParams& p, const ItemSpan& 
   return p.whole_items ? (s.nt > 0) : s.nt;
 }
 
-template <int ROWS, int KT, int NT>
+template <int ROWS, int KT, int NT, bool READ_ONLY = false>
 __device__ Run find_run(const PagedParams& p, int row_tiles, int min_tiles, Run* run_sh, long long* sh) {
   constexpr int W = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -128,7 +128,7 @@ __device__ Run find_run(const PagedParams& p, int row_tiles, int min_tiles, Run*
   for (int i = first, b = -1; i < last; ++i) {
     SeqLen s;
     if (i / row_tiles != b) b = i / row_tiles;
-    s = seq_lens(p, b);
+    s = seq_lens<READ_ONLY>(p, b);
     sum += line_tiles(p, item_span<ROWS, KT>(p, s.n, s.kv, i - b * row_tiles));
   }
   long long inc = sum;
@@ -155,7 +155,7 @@ __device__ Run find_run(const PagedParams& p, int row_tiles, int min_tiles, Run*
   if (s0 < s1 && s0 >= at && s0 < at + sum * p.Hkv) {
     for (int i = first; i < last; ++i) {
       const int b = i / row_tiles;
-      const SeqLen s = seq_lens(p, b);
+      const SeqLen s = seq_lens<READ_ONLY>(p, b);
       const int nt = line_tiles(p, item_span<ROWS, KT>(p, s.n, s.kv, i - b * row_tiles));
       const long long w = (long long)nt * p.Hkv;
       if (s0 < at + w) {
@@ -179,13 +179,13 @@ struct Piece {
 };
 
 // Next piece of the run; r.left > 0 on entry.
-template <int ROWS, int KT>
+template <int ROWS, int KT, bool READ_ONLY = false>
 __device__ __forceinline__ Piece next_piece(const PagedParams& p, int row_tiles, Run& r) {
   Piece q;
   for (;;) {
     q.b = r.idx / row_tiles;
     q.rt = r.idx - q.b * row_tiles;
-    const SeqLen s = clamp_lens(p, p.n_new ? __ldg(p.n_new + q.b) : p.N, __ldg(p.kv_len + q.b));
+    const SeqLen s = seq_clamped<READ_ONLY>(p, q.b);
     q.n = s.n;
     q.kv = s.kv;
     q.s = item_span<ROWS, KT>(p, s.n, s.kv, q.rt);

@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  Run run = find_run<ROWS, kTileKeys, C::THREADS>(p, row_tiles, kTilesMin, run_sh, scan_sh);  // block barriers
+  Run run = find_run<ROWS, kTileKeys, C::THREADS, kReadOnly>(p, row_tiles, kTilesMin, run_sh, scan_sh);  // block barriers
   tc_fence_after();
   const uint32_t tmem = misc[0];
 
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
       int pc = 0;
       bool ok = true;
       for (; run.left > 0 && ok; ++pc) {
-        const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
+        const Piece q = next_piece<ROWS, kTileKeys, kReadOnly>(p, row_tiles, run);
         if (pc > 0) {  // the slots are free, and their last tiles have landed
           ok = wait(q_empty, pc - 1);
           for (int w = 0; w < (SPLIT ? 1 : 2); ++w) ok = ok && wait(&q_full[w], pc - 1);
@@ -316,14 +316,14 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
         int c = 0, k = 0;
         bool ok = true;
         while (run.left > 0 && ok) {
-          const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
+          const Piece q = next_piece<ROWS, kTileKeys, kReadOnly>(p, row_tiles, run);
           const TileNeed<SPLIT> need(p, q);
           // lane l < 2 sub holds the table entry of tokens l per .. of a tile;
           // the next tile's is on its way while this one's pieces wait
           auto keeps = [&](int j) { return j < q.s.hi && j + per > q.s.lo; };
           auto entry_of = [&](int kt) {
             const int j = kt * kTileKeys + lane * per;
-            return lane < 2 * sub && keeps(j) ? table_entry(p, q.b, j) : 0;
+            return lane < 2 * sub && keeps(j) ? table_entry<kReadOnly>(p, q.b, j) : 0;
           };
           int next = entry_of(q.s.t0 + q.t);
           for (int i = 0; i < q.m && ok; ++i) {
@@ -378,16 +378,16 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
         int k = 0, landed = 0;
         bool ok = true;
         while (run.left > 0 && ok) {
-          const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
+          const Piece q = next_piece<ROWS, kTileKeys, kReadOnly>(p, row_tiles, run);
           const TileNeed<SPLIT> need(p, q);
           int j0 = (q.s.t0 + q.t) * kTileKeys + part * per;  // first token of this lane's copies
           auto keeps = [&](int j) { return part < sub && role < 2 && j < q.s.hi && j + per > q.s.lo; };
-          int next = keeps(j0) ? table_entry(p, q.b, j0) : 0;
+          int next = keeps(j0) ? table_entry<kReadOnly>(p, q.b, j0) : 0;
           for (int i = 0; i < q.m; ++i, j0 += kTileKeys) {
             const int kt = q.s.t0 + q.t + i;
             const bool mine = keeps(j0);
             const int entry = next;  // the next tile's is on its way while this one waits for its stage
-            next = i + 1 < q.m && keeps(j0 + kTileKeys) ? table_entry(p, q.b, j0 + kTileKeys) : 0;
+            next = i + 1 < q.m && keeps(j0 + kTileKeys) ? table_entry<kReadOnly>(p, q.b, j0 + kTileKeys) : 0;
             if (need.mask(kt) == 0) continue;
             const int st = k % S, key0 = kt * kTileKeys;
             if (k >= S) ok = wait(&empty[st], k / S - 1);
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
       // in `cur`; with a copy a call this loop outgrew the instruction cache
       // (ragged chunks 342 -> 275 us). bf16 has room for a copy a row tile.
       for (; run.left > 0 && ok; ++pc) {
-        const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
+        const Piece q = next_piece<ROWS, kTileKeys, kReadOnly>(p, row_tiles, run);
         const TileNeed<SPLIT> need(p, q);
         for (int w = 0; w < (SPLIT ? 1 : 2) && ok; ++w) ok = wait(E4M3 ? &q_ready[w] : &q_full[w], pc);
         cur.fresh = oth.fresh = true;
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
     SplitItem split{0, 0, 0, 0};
     for (; run.left > 0; ++pc) {
       const long long at = run.pos;
-      const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
+      const Piece q = next_piece<ROWS, kTileKeys, kReadOnly>(p, row_tiles, run);
       if (q.t == 0 && q.m < q.s.nt)
         split = SplitItem{q.b * row_tiles + q.rt, q.hk, run_of(run.total, at + q.s.nt - 1, run.ctas) - (int)blockIdx.x + 1, 0};
       const TileNeed<SPLIT> need(p, q);
@@ -932,7 +932,7 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
       int c = 0, k = 0;
       bool ok = true;
       while (run.left > 0 && ok) {
-        const Piece q = next_piece<ROWS, kTileKeys>(p, row_tiles, run);
+        const Piece q = next_piece<ROWS, kTileKeys, kReadOnly>(p, row_tiles, run);
         const TileNeed<SPLIT> need(p, q);
         float sig = 0x1p-112f;
         for (int i = 0; i < q.m && ok; ++i) {
@@ -1050,7 +1050,7 @@ __global__ void __launch_bounds__(256) paged_join_tiles_kernel(const PagedParams
   const SplitItem it = wk.split[blockIdx.x];
   if (it.parts <= 1) return;
   const int b = it.idx / row_tiles, rt = it.idx - b * row_tiles;
-  const SeqLen s = clamp_lens(p, p.n_new ? __ldg(p.n_new + b) : p.N, __ldg(p.kv_len + b));
+  const SeqLen s = seq_clamped(p, b);
   const int x = blockIdx.y * 256 + threadIdx.x;
   const int r = x % ROWS, c0 = x / ROWS;  // channel groups c0, c0 + 2048 / ROWS, ...
   const int R = rt * ROWS + r;
@@ -1100,7 +1100,7 @@ __global__ void __launch_bounds__(256) paged_join_parts_kernel(const PagedParams
   if (it.parts <= 1) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = it.idx / row_tiles, rt = it.idx - b * row_tiles;
-  const SeqLen s = clamp_lens(p, p.n_new ? __ldg(p.n_new + b) : p.N, __ldg(p.kv_len + b));
+  const SeqLen s = seq_clamped(p, b);
   const int r = (blockIdx.y % (ROWS / 32)) * 32 + lane, c0 = blockIdx.y / (ROWS / 32) * 4;
   const int R = rt * ROWS + r;
   const bool written = R < p.G * p.N && R - fdiv(R, p.f_n) * p.N < s.n;

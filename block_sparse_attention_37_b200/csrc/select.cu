@@ -133,10 +133,10 @@ __global__ void __launch_bounds__(256) select_kernel(SelectParams p) {
         const int J = J0 + 8 * r;
         const float* kr = kb + (size_t)(J < p.nKB ? J : 0) * D + lane * PL;
         if constexpr (PL == 4) {
-          const float4 k4 = __ldg(reinterpret_cast<const float4*>(kr));
+          const float4 k4 = *reinterpret_cast<const float4*>(kr);
           kv[r][0] = k4.x; kv[r][1] = k4.y; kv[r][2] = k4.z; kv[r][3] = k4.w;
         } else {
-          const float2 k2 = __ldg(reinterpret_cast<const float2*>(kr));
+          const float2 k2 = *reinterpret_cast<const float2*>(kr);
           kv[r][0] = k2.x; kv[r][1] = k2.y;
         }
       }
@@ -298,10 +298,10 @@ __global__ void __launch_bounds__(256) select_rows_kernel(SelectParams p) {
         const float* kr = kb + (size_t)J * D + lane * PL;
         float a = 0.f;
         if constexpr (PL == 4) {
-          const float4 k4 = __ldg(reinterpret_cast<const float4*>(kr));
+          const float4 k4 = *reinterpret_cast<const float4*>(kr);
           a = fmaf(qr[0], k4.x, fmaf(qr[1], k4.y, fmaf(qr[2], k4.z, qr[3] * k4.w)));
         } else {
-          const float2 k2 = __ldg(reinterpret_cast<const float2*>(kr));
+          const float2 k2 = *reinterpret_cast<const float2*>(kr);
           a = fmaf(qr[0], k2.x, qr[1] * k2.y);
         }
         acc[i] = a;
@@ -396,7 +396,8 @@ cudaError_t launch_block_pool(int d, const PoolParams& p, cudaStream_t stream) {
 
 // A programmatic dependent launch: the selection grid may be scheduled while
 // the kernel before it (pooling or the score pass) finishes; its kernels
-// wait on griddepcontrol.wait before reading anything that kernel wrote.
+// wait on griddepcontrol.wait before reading anything that kernel wrote, and
+// read it by ordinary loads (the read-only path is not ordered by the wait).
 template <class K>
 static cudaError_t launch_dependent(K kernel, unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
                                    const SelectParams& p) {
