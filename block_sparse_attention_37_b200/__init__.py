@@ -378,13 +378,29 @@ def forward_fp8(dm: Dims, ops: Fp8Operands, o, head_mode, blocks: BlockList | No
                                   _stream(stream)), "bsa_forward_fp8")
 
 
+def _held(name):
+    """A property over the slot `_name`: the tensor may be written (cache.kv_len += 1), not replaced."""
+    def get(self):
+        return getattr(self, "_" + name)
+
+    def put(self, t):
+        if t is not getattr(self, "_" + name):
+            raise AttributeError(f"a PagedCache keeps its tensors: write into {name} in place (copy_, +=), or build "
+                                 f"another PagedCache")
+    return property(get, put)
+
+
 class PagedCache:
     """Keys and values of several sequences in pages (see bsa_paged_cache): k and v are cuda
     [n_pages, Hkv, page, d] bf16, or uint8 e4m3 codes with the fp32 scales k_scale and v_scale
     [n_pages, Hkv, page]; table is int32 [B, max_pages], kv_len int32 [B]. The tensors are the
-    caller's: their contents may change between calls (pages filled, kv_len raised), the tensors
-    of a PagedCache may not."""
-    __slots__ = ("k", "v", "table", "kv_len", "k_scale", "v_scale", "device", "_c", "_ref", "_index", "_B", "_Hkv")
+    caller's: their contents may change between calls (pages filled, kv_len raised). Replacing one
+    (cache.kv_len = cache.kv_len + 1) is refused, and so is a call once one of them lies elsewhere
+    in memory than it did (set_, a resized storage)."""
+    __slots__ = ("_k", "_v", "_table", "_kv_len", "_k_scale", "_v_scale", "device", "_c", "_ref", "_index", "_B", "_Hkv",
+                 "_where", "_at")
+    k, v, table, kv_len = _held("k"), _held("v"), _held("table"), _held("kv_len")
+    k_scale, v_scale = _held("k_scale"), _held("v_scale")
 
     def __init__(self, k, v, table, kv_len, k_scale=None, v_scale=None):
         e4m3 = isinstance(k, torch.Tensor) and k.dtype == torch.uint8
@@ -415,8 +431,10 @@ class PagedCache:
         for t, name in ((v, "v"), (table, "table"), (kv_len, "kv_len"), (k_scale, "k_scale"), (v_scale, "v_scale")):
             if t is not None and t.device != k.device:
                 raise ValueError(f"{name} is on {t.device}, k on {k.device}")
-        self.k, self.v, self.table, self.kv_len = k, v, table, kv_len
-        self.k_scale, self.v_scale, self.device = k_scale, v_scale, k.device
+        self._k, self._v, self._table, self._kv_len = k, v, table, kv_len
+        self._k_scale, self._v_scale, self.device = k_scale, v_scale, k.device
+        self._where = tuple(t.data_ptr for t in (k, v, table, kv_len, k_scale, v_scale) if t is not None)
+        self._at = [where() for where in self._where]
         self._c = PagedCacheC(CACHE_E4M3 if e4m3 else CACHE_BF16, n_pages, Hkv, page, d, table.shape[1], *p)
         self._ref, self._index, self._B, self._Hkv = ctypes.byref(self._c), k.get_device(), table.shape[0], Hkv
 
@@ -433,10 +451,13 @@ class PagedCache:
                    torch.zeros((B,), dtype=torch.int32, device=device), sc(), sc())
 
     def _chunk(self, dm: Dims) -> int:
-        """Elements of one head of this call's chunk, B * N * d; refuses dims that are not the cache's."""
+        """Elements of one head of this call's chunk, B * N * d; refuses dims that are not the cache's,
+        and a cache whose tensors no longer lie where the library was told."""
         B = dm.B
         if B != self._B:
             raise ValueError(f"dims hold {B} sequences, the cache's table {self._B}")
+        if [where() for where in self._where] != self._at:
+            raise ValueError("a tensor of this PagedCache was moved or resized: build another PagedCache")
         return B * max(dm.N, 0) * max(dm.d, 0)
 
 
