@@ -668,6 +668,7 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
           *mx_mine = __uint_as_float(top);
           named_bar(1 + w, 256);  // every row is read: at d = 64 the two forms lie elsewhere
           top = max(top, __float_as_uint(*mx_other));
+          named_bar(pair_bar, 64);  // read: a piece without tiles goes on to its sums in the same word
           // 2^(7 - e), e the exponent of the largest value, kept in the normal range
           const int ex = min(max((int)(top >> 7), 8), 253);
           const float down = __int_as_float((261 - ex) << 23);
