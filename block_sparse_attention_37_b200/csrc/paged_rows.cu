@@ -203,8 +203,9 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
         __syncwarp();
       }
     }
-    // copies in flight land before the CTA ends (an aborting CTA's consumers may not wait for them)
-    if (*abort_flag && lane == 0)
+    // copies in flight land before the CTA ends, whether or not it aborts:
+    // consumers may give up on them after this warp is through
+    if (lane == 0)
       for (int t = max(0, k - S); t < k; ++t)
         if (t != p.withhold_tile) mbar_drain(&full[t % S], (uint32_t)(t / S) & 1u);
     return;
@@ -230,6 +231,7 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
   float* sm_l = sm_m + W * 8 * R8;
   const int rows = p.G * p.N;
   int k = 0;  // tiles of the run before this piece
+  bool ok = true;
   SplitItem split{0, 0, 0, 0};
   while (run.left > 0) {
     const long long at = run.pos;
@@ -306,13 +308,16 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
     float sigma = 0x1p-112f, rs = kRowsGain / 0x1p-112f;
 
     // the group's tiles: every NG-th of the run
-    for (int it = (grp + NG - k % NG) % NG; it < q.m; it += NG) {
+    for (int it = (grp + NG - k % NG) % NG; ok && it < q.m; it += NG) {
       const int st = (k + it) % S;
       const int key0 = (q.s.t0 + q.t + it) * kRowsKeys;
       const bool edge = key0 < q.s.clo || key0 + kRowsKeys > q.s.chi;
-      if (!warp_all(mbar_wait(&full[st], (uint32_t)((k + it) / S) & 1u, abort_flag, p.wait_limit_ns))) {
+      ok = warp_all(mbar_wait(&full[st], (uint32_t)((k + it) / S) & 1u, abort_flag, p.wait_limit_ns));
+      if (!ok) {
         // every warp sees the flag in its next wait; all go on to the same
-        // block barriers, so none is left behind in one (the output is void)
+        // block barriers, so none is left behind in one (the output is void).
+        // This warp takes no further tile: an arrival out of turn would let
+        // the producer load over a copy in flight
         cta_fail(abort_flag, BSA_DEVERR_TIMEOUT);
         break;
       }

@@ -305,7 +305,9 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
           }
         __syncwarp();
       }
-      if (*abort_flag && pc > 0 && lane == 0)
+      // here and in the producers below: copies in flight land before the CTA
+      // ends, whether or not it aborts (the softmax may yet give up on them)
+      if (pc > 0 && lane == 0)
         for (int w = 0; w < (SPLIT ? 1 : 2); ++w) mbar_drain(&q_full[w], (uint32_t)(pc - 1) & 1u);
     } else if (warp == 2 && E4M3) {
       if constexpr (E4M3) {
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
             ++k;
           }
         }
-        if (*abort_flag && lane == 0)
+        if (lane == 0)
           for (int t = max(0, c - C::RAW); t < c; ++t) mbar_drain(&raw_full[t % C::RAW], (uint32_t)(t / C::RAW) & 1u);
       }
     } else if (warp == 0 || warp == 2) {
@@ -442,9 +444,8 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
             ++k;
           }
         }
-        // copies in flight land before the CTA ends; a stage whose tile was
-        // cleared by this warp has landed already
-        if (*abort_flag && lane == 0) {
+        // a stage whose tile was cleared by this warp has landed already
+        if (lane == 0) {
           for (int t = max(0, k - S); t < k; ++t)
             if (!IS_K || t != p.withhold_tile) mbar_drain(&full[t % S], (uint32_t)(t / S) & 1u);
           if constexpr (E4M3)
@@ -510,6 +511,7 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
                          std::make_integer_sequence<int, D / 16>{});
                   tc_commit_warp(&s_full[w]);
                 }
+                if (!ok) break;
                 tc_commit_warp(&k_empty[ks]);
                 ++cur.np;
                 ++oth.np;
@@ -602,7 +604,8 @@ __global__ void __launch_bounds__(TilesCfg<D, E4M3, SPLIT>::THREADS, 1)
             oth = t;
           }
           if (!flush) {
-            tc_commit_warp(&k_empty[st]);
+            // (a stage whose tile was waited for in vain is not free: its copies may be in flight)
+            if (ok) tc_commit_warp(&k_empty[st]);
             ++k;
           }
         }

@@ -4,9 +4,9 @@ The agents follow paged_tiles_kernel's code: the producers of Q, K and V (bf16: 
 rows it clears; e4m3: code pieces and their converters), the MMA issuer with its long-run loop, and
 the softmax warps, two (a row's column halves) in a pair. mbarriers are modelled by their completed
 phases and the one-bit parity test; copies land in any order, MMAs and commits complete in issue
-order. Checked:
+order. In half of the runs waits give up at random, as when a wait limit runs out. Checked:
 
-* no deadlock;
+* no deadlock, in an aborting CTA either;
 * every read finds its own tile, piece or exchanged value: Q, K, V, V codes and scales, K scales,
   sigma, S, P, O, the word that a row's two warps exchange;
 * nothing is loaded over a copy in flight or an operand that an issued MMA still reads, no barrier is
@@ -14,8 +14,9 @@ order. Checked:
 * when the CTA ends no copy and no MMA is in flight.
 
 Planted mistakes, each of which the model must see: a shorter scale ring, no flush of the PV that
-holds up a V stage, the row tiles always in one order, and no barrier between the two uses of the
-exchange word. Stage counts and the form of the last are read from the kernel's source."""
+holds up a V stage, the row tiles always in one order, drains only of a CTA that has already
+aborted, stages released by a failed wait, and no barrier between the two uses of the exchange word.
+Stage counts and the forms of the last three are read from the kernel's source."""
 import os
 import random
 import re
@@ -609,9 +610,22 @@ def test_every_schedule_ends_and_reads_its_own(d, e4m3, split):
         assert (seed, _outcome(d, e4m3, split, seed)) == (seed, "ok")
 
 
+@pytest.mark.parametrize("d,e4m3,split", CONFIGS)
+def test_a_cta_that_gives_up_ends_without_anything_in_flight(d, e4m3, split):
+    for seed in range(100):
+        assert (seed, _outcome(d, e4m3, split, seed, aborts=True)) == (seed, "ok")
+
+
+@pytest.mark.parametrize("d,e4m3,split", CONFIGS)
+def test_a_withheld_tile_ends_without_anything_in_flight(d, e4m3, split):
+    for seed in range(60):
+        assert (seed, _outcome(d, e4m3, split, seed, aborts=True, withhold=seed % 7)) == (seed, "ok")
+
+
 PLANTS = [  # mistake, configuration, with waits that give up, what shows it
     ("short ring", (128, True, False), False, ""), ("no flush", (128, False, False), False, ""),
-    ("one order", (128, False, False), False, ""), ("word_barrier", (128, True, False), False, "exchange word")]
+    ("one order", (128, False, False), False, ""), ("always_drain", (64, True, True), True, "in flight at the end"),
+    ("commit_if_ok", (128, False, False), True, "in flight"), ("word_barrier", (128, True, False), False, "exchange word")]
 
 
 @pytest.mark.parametrize("plant,cfg,aborts,shows", PLANTS, ids=[p[0] for p in PLANTS])
