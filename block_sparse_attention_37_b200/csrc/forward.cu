@@ -622,9 +622,10 @@ __global__ void __launch_bounds__(384, 1)
         }
         issued = t + 1;
       }
-      if (*abort_flag)  // copies in flight land before the CTA ends
-        for (int t = issued - S < 0 ? 0 : issued - S; t < issued; ++t)
-          if (!IS_K || t != p.withhold_tile) mbar_drain(&full[t % S], (uint32_t)(t / S) & 1u);
+      // copies in flight land before the CTA ends, whether or not it aborts (a
+      // consumer may give up on them after this loop)
+      for (int t = issued - S < 0 ? 0 : issued - S; t < issued; ++t)
+        if (!IS_K || t != p.withhold_tile) mbar_drain(&full[t % S], (uint32_t)(t / S) & 1u);
     };
     if (lane == 0 && T > 0) {
       if (warp == 0)

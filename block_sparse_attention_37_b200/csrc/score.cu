@@ -129,10 +129,10 @@ __global__ void __launch_bounds__(192, 2)
                         t * 128 + 64 * r, bh);
         issued = t + 1;
       }
-      if (*abort_flag) {  // copies in flight land before the CTA ends
-        mbar_drain(q_full, 0u);
-        for (int t = issued - S < 0 ? 0 : issued - S; t < issued; ++t) mbar_drain(&k_full[t % S], (uint32_t)(t / S) & 1u);
-      }
+      // copies in flight land before the CTA ends, whether or not it aborts (a
+      // consumer may give up on them after this loop)
+      mbar_drain(q_full, 0u);
+      for (int t = issued - S < 0 ? 0 : issued - S; t < issued; ++t) mbar_drain(&k_full[t % S], (uint32_t)(t / S) & 1u);
     }
   } else if (warp == 1) {
     if (lane == 0) {

@@ -11,6 +11,7 @@ import re
 
 import pytest
 
+from test_abort_drains import drains_behind_the_flag
 from test_paged_ring import _rows_layouts
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "block_sparse_attention_37_b200", "csrc")
@@ -18,7 +19,7 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
 
 def source_forms():
     code = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, "paged_rows.cu")).read())
-    return {"always_drain": not re.search(r"if \(\*abort_flag[^;{]*\{?[^;]*mbar_drain", code),
+    return {"always_drain": not drains_behind_the_flag(code),
             "dead_warps_stay_dead": bool(re.search(r"bool ok = true;\s*SplitItem split", code))
             and bool(re.search(r"for \(int it = [^;]+; ok && it < q\.m;", code))}
 

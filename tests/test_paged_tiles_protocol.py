@@ -23,6 +23,8 @@ import re
 
 import pytest
 
+from test_abort_drains import drains_behind_the_flag
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "block_sparse_attention_37_b200", "csrc")
 SRC = open(os.path.join(CSRC, "paged_tiles.cu")).read()
 
@@ -65,7 +67,7 @@ def config(d, e4m3, split):
 def source_forms():
     """How the kernel is written, for the mistakes that were once in it."""
     code = re.sub(r"//[^\n]*", "", SRC)
-    return {"always_drain": not re.search(r"if \(\*abort_flag[^;{]*\{?[^;]*mbar_drain", code),
+    return {"always_drain": not drains_behind_the_flag(code),
             "commit_if_ok": bool(re.search(r"if \(ok\) tc_commit_warp\(&k_empty\[st\]\)", code))
             and bool(re.search(r"if \(!ok\) break;\s*tc_commit_warp\(&k_empty\[ks\]\)", code)),
             "word_barrier": bool(re.search(r"top = max\(top, __float_as_uint\(\*mx_other\)\);\s*named_bar\(pair_bar, 64\);", code))}
