@@ -84,12 +84,14 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const PagedParams p) 
         k[w] = reinterpret_cast<const uint4*>(p.new_k)[(r * LANES + l) * W + w];
         v[w] = reinterpret_cast<const uint4*>(p.new_v)[(r * LANES + l) * W + w];
       }
-      const int j = s.kv - s.n + n;
-      if (j < 0) {
+      // the position by the length as given: one that runs past the table
+      // must not move the chunk over tokens that are there
+      const long long j = (long long)p.kv_len[b] - s.n + n;
+      if (j < 0 || j >= (long long)p.max_pages << p.page_log2) {
         record_error(BSA_DEVERR_BAD_INDEX);
       } else {
-        const int pg = page_of(p, b, j);
-        if (pg >= 0) dst = cache_row(p, pg, hk, j);
+        const int pg = page_of(p, b, (int)j);
+        if (pg >= 0) dst = cache_row(p, pg, hk, (int)j);
       }
     }
   }

@@ -288,7 +288,8 @@ int bsa_forward_fp8(const bsa_dims* dims, const uint8_t* q8, const uint8_t* k8, 
  * index outside [0, n_pages) where a page is needed (append drops the token,
  * read gives zeros, the forward reads page 0 in its place), kv_len outside
  * [0, max_pages * page], n_new outside [0, N], n_new above kv_len for an
- * append, begin below 0 (clamped; append drops tokens at negative positions).
+ * append, begin below 0 (clamped; append drops tokens whose positions are
+ * negative or past the table, and writes the others).
  * Slots at or past kv_len[b], and pages that hold no kept token, may hold
  * anything, NaN included; V of a token below kv_len[b] must be finite unless
  * every row of the chunk may turn NaN. */
