@@ -475,14 +475,20 @@ def _paged_ptr(cache: PagedCache, t, dtype, name, numel):
     return p
 
 
+# The current device and a device's current stream by its raw handle: torch's own short ways to them
+# where it has them, which the paged calls' host time shows, else the public ones.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _paged_call(cache: PagedCache, name: str, stream, *args):
     """The library call `name` with the cache's device current, on `stream` or that device's
     current stream (asked for by its raw handle: a torch Stream object costs as much as a launch)."""
     i = cache._index
-    if i >= 0 and i != torch._C._cuda_getDevice():
+    if i >= 0 and i != _current_device():
         with torch.cuda.device(i):
             return _paged_call(cache, name, stream, *args)
-    raw = torch._C._cuda_getCurrentRawStream(i) if stream is None and i >= 0 else _stream(stream)
+    raw = _raw_stream(i) if stream is None and i >= 0 else _stream(stream)
     status = getattr(_lib(), name)(*args, raw)
     if status != OK:
         raise BsaError(status, name)
@@ -510,7 +516,7 @@ def paged_read(dm: Dims, cache: PagedCache, k, v, begin=None, stream=None):
 def paged_workspace_size(dm: Dims, cache: PagedCache) -> int:
     """Bytes of device workspace paged_forward needs for these dims and cache on the cache's device,
     whatever the lengths."""
-    if getattr(cache, "_index", -1) >= 0 and cache._index != torch._C._cuda_getDevice():
+    if getattr(cache, "_index", -1) >= 0 and cache._index != _current_device():
         with torch.cuda.device(cache._index):
             return paged_workspace_size(dm, cache)
     return int(_lib().bsa_paged_workspace_size(ctypes.byref(dm), cache._ref))

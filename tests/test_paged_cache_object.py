@@ -68,3 +68,24 @@ def test_moved_tensors_are_refused_by_every_call(recorded, e4m3, how):  # noqa: 
             with pytest.raises(ValueError, match="moved or resized"):
                 call()
         assert not rec.calls, name
+
+
+def test_a_torch_without_its_short_ways_to_device_and_stream_will_do():
+    """The binding falls back to torch's public functions (a process of its own: the module is imported
+    after the private names are gone)."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+torch.cuda.current_device = lambda: 3
+torch.cuda.current_stream = lambda i=None: type("S", (), {"cuda_stream": 1000 + i})
+import block_sparse_attention_37_b200 as m
+assert m._current_device() == 3 and m._raw_stream(2) == 1002
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert out.returncode == 0, out.stderr
