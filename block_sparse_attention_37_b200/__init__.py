@@ -458,7 +458,7 @@ class PagedCache:
             raise ValueError(f"dims hold {B} sequences, the cache's table {self._B}")
         if [where() for where in self._where] != self._at:
             raise ValueError("a tensor of this PagedCache was moved or resized: build another PagedCache")
-        return B * max(dm.N, 0) * max(dm.d, 0)
+        return B * dm.N * dm.d  # (a negative dimension is the library's to refuse)
 
 
 def _paged_ptr(cache: PagedCache, t, dtype, name, numel):
@@ -531,7 +531,7 @@ def paged_forward(dm: Dims, cache: PagedCache, q, o, workspace, n_new=None, caus
     the last `window` of them; otherwise every cached token. workspace: cuda tensor of at least
     paged_workspace_size bytes, 256-byte aligned, not shared with a call that may overlap; scale
     defaults to 1/sqrt(d)."""
-    n = cache._chunk(dm) * max(dm.H, 0)
+    n = cache._chunk(dm) * dm.H
     wp = _paged_ptr(cache, workspace, getattr(workspace, "dtype", None), "workspace", 0)
     _paged_call(cache, "bsa_paged_forward", stream, ctypes.byref(dm), _paged_ptr(cache, q, torch.bfloat16, "Q", n),
                 _paged_ptr(cache, n_new, torch.int32, "n_new", cache._B) if n_new is not None else None, cache._ref,

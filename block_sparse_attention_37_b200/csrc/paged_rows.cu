@@ -251,8 +251,9 @@ __global__ void __launch_bounds__(RowsCfg<D, E4M3, R8, NG>::THREADS, 2)
     }
     // Q as B fragments, row g of each eight. bf16: k-step s covers channels
     // 16 s .. 16 s + 15 in order. e4m3: fp16 after a power-of-two scale of
-    // the row (exact down to 2^-24 of its largest value), in the order in
-    // which a lane's 16-byte reads of K deliver the channels (see below).
+    // the row (exact down to 2^-17 of its largest value, an error of at most
+    // 2^-25 of it below), in the order in which a lane's 16-byte reads of K
+    // deliver the channels (see below).
     uint32_t qf[R8][D / 16][2];
     float zs[NR];  // row factor of the logits
 #pragma unroll

@@ -25,7 +25,7 @@
 // e4m3: QK^T runs on K's codes as they are (kind::f8f6f4, twice the 16-bit
 // rate): each row of Q, scaled by a power of two, is the sum of two e4m3
 // values, its rounding and the rest, which hold bf16's eight bits exactly down
-// to 2^-9 of the row's largest value (2^-18 of it is the error below that), so
+// to 2^-9 of the row's largest value (2^-17 of it bounds the error below), so
 // two products give the logits and take the time of one in bf16. K's scale
 // multiplies the logits. PV runs in fp16: V is code times (scale / sigma), the
 // quotient rounded to 11 bits and the product once more (sigma a power of two,

@@ -292,7 +292,8 @@ int bsa_forward_fp8(const bsa_dims* dims, const uint8_t* q8, const uint8_t* k8, 
  * negative or past the table, and writes the others).
  * Slots at or past kv_len[b], and pages that hold no kept token, may hold
  * anything, NaN included; V of a token below kv_len[b] must be finite unless
- * every row of the chunk may turn NaN. */
+ * every row of the chunk may turn NaN (a masked weight of zero times NaN; which
+ * rows do turn depends on the tiles). */
 #define BSA_CACHE_BF16 1
 #define BSA_CACHE_E4M3 2
 
@@ -344,15 +345,23 @@ size_t bsa_paged_workspace_size(const bsa_dims* dims, const bsa_paged_cache* cac
  *  o = softmax(scale * q.k) V over the kept keys, fp32 accumulation, the
  *  weights rounded to 16 bits for the product with V, o rounded to bf16;
  *  a row that keeps no key gives 0. Rows i >= n_new[b] of O are left as they were.
- *  What is rounded before the products: the weights, to bf16 (bf16 cache), or to
- *  fp16 (e4m3 cache), there with the token's V scale (up to 16 rows a key/value
- *  head) or beside V values rounded twice to 11 bits (more rows); and, for an e4m3
- *  cache and more than 16 rows, Q: exact down to 2^-9 of its row's largest value,
- *  with an error of 2^-18 of that value below. Codes and K scales are not.
- *  V in an e4m3 cache is held over the largest V scale among the tokens of values
- *  (not all zeros) that any row of the same tile keeps: tokens with V scales down
- *  to 2^-20 of it keep their bits, smaller ones lose them, and where a weight
- *  times the scale is below 2^-36 of it the token adds nothing.
+ *  Rounded before the products, beside the weights (to bf16; to fp16 for an
+ *  e4m3 cache), with R = N * H / Hkv rows a key/value head:
+ *   - bf16 cache: nothing.
+ *   - e4m3 cache, R <= 16: Q, exact down to 2^-17 of its row's largest value,
+ *     with an error of at most 2^-25 of that value below; the weight and its
+ *     token's V scale, one product rounded to 11 bits.
+ *   - e4m3 cache, R > 16: Q, exact down to 2^-9 of its row's largest value, with
+ *     an error of at most 2^-17 of that value below; V, its scale and then its
+ *     value each rounded to 11 bits.
+ *   K's codes and scales are used as they are.
+ *  e4m3 cache: V's scales are held over the largest one among the tokens (all
+ *  zeros excepted) that rows of the same tile keep. Tokens with scales down to
+ *  2^-20 of it keep the bits named above, smaller ones lose some, and a weight
+ *  times its scale below 2^-36 of it counts as zero.
+ *  In a batch with n_new much below N, rows pack badly: a key/value head's rows
+ *  are laid out head by head (row h * N + i), so K and V of such a sequence may
+ *  be read up to H / Hkv times.
  *  dims: B, H, N and d are read. Q, O: device bf16 [B, H, N, d].
  *  window: 0 for none; needs causal = 1. scale: finite and positive.
  *  workspace: device, at least bsa_paged_workspace_size bytes, 256-byte
