@@ -32,7 +32,9 @@ namespace bsa {
 
 constexpr int kRowsTile = 16;     // query rows of an item
 constexpr int kRowsKeys = 64;     // keys of a tile
-constexpr int kRowsMinTiles = 2;  // a run is at least this many tiles
+// A run is at least this many tiles (one token, 16 heads, 437 to 20,000 keys:
+// 1 gives within 2% of it, 4 is up to 7% slower).
+constexpr int kRowsMinTiles = 2;
 constexpr float kRowsTau = 3.f;   // the state moves when a row's maximum grows by more than 2^3
 constexpr float kRowsGain = 4096.f;  // e4m3: weights (at most 2^3) are held times this in fp16
 

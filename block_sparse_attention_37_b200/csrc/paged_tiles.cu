@@ -43,7 +43,9 @@
 namespace bsa {
 
 constexpr int kTileKeys = 128;
-constexpr int kTilesMin = 4;  // a run is at least this many tiles
+// A run is at least this many tiles (one sequence of 437 to 20,000 keys, 32
+// and 300 rows: 2 gives 10% less to 5% more, 8 up to 60% more).
+constexpr int kTilesMin = 4;
 
 template <int D, bool E4M3, bool SPLIT>
 struct TilesCfg {
