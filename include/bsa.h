@@ -356,9 +356,10 @@ size_t bsa_paged_workspace_size(const bsa_dims* dims, const bsa_paged_cache* cac
  *     value each rounded to 11 bits.
  *   K's codes and scales are used as they are.
  *  e4m3 cache: V's scales are held over the largest one among the tokens (all
- *  zeros excepted) that rows of the same tile keep. Tokens with scales down to
- *  2^-20 of it keep the bits named above, smaller ones lose some, and a weight
- *  times its scale below 2^-36 of it counts as zero.
+ *  zeros excepted) that rows of the same query tile keep. Tokens with scales to
+ *  2^-20 of it keep the bits named above, smaller ones lose some. A weight
+ *  (R <= 16: times its scale over that largest one) keeps 11 bits down to 2^-26
+ *  of its row's largest, fewer below, and counts as zero under 2^-37.
  *  In a batch with n_new much below N, rows pack badly: a key/value head's rows
  *  are laid out head by head (row h * N + i), so K and V of such a sequence may
  *  be read up to H / Hkv times.
